@@ -41,14 +41,15 @@
  *     are independent.
  *   - Weights are static data.  The matmul calls (bnn_binary_gemm*,
  *     bnn_binary_linear, bnn_ternary_gemm*, bnn_ternary_linear,
- *     bnn_ternary_sparse_gemm) are launched with programmatic dependent
- *     launch: they may start, and read their WEIGHT operands (packed sign or
- *     trit rows; the sparse row_ptr and entries), while the kernel before them
+ *     bnn_ternary_sparse_gemm, bnn_fp8_gemm, bnn_fp8_grouped_gemm) are launched
+ *     with programmatic dependent launch: they may start, and read their WEIGHT
+ *     operands (packed sign, trit or e4m3 rows and the e4m3 blocks' scales; the
+ *     sparse row_ptr and entries), while the kernel before them
  *     on the stream is still running.  Activations, scales, biases and outputs
  *     keep plain stream order.  So a weight operand must be complete before
  *     the stream reaches the matmuls that read it: after preparing it (with
  *     bnn_pack_signs, bnn_ternary_pack*, bnn_ternary_sparse_encode,
- *     bnn_tbin_load_ternary or any other kernel), synchronise the stream or
+ *     bnn_tbin_load_ternary, bnn_fp8_pack_weight or any other kernel), synchronise the stream or
  *     the device, or prepare it on another stream and make this one wait on
  *     an event recorded there.  Activations packed or produced right before a
  *     matmul on the same stream need nothing.
@@ -405,6 +406,106 @@ bnn_status bnn_tbin_load_ternary(const uint8_t* file_dev, uint64_t len, const bn
 /* bnn_tbin_load_raw -- a raw float16 record's data as float32 [data_elems]. */
 bnn_status bnn_tbin_load_raw(const uint8_t* file_dev, uint64_t len, const bnn_tbin_record* rec, float* out,
                              cudaStream_t s);
+
+/*
+ * 8-bit block-scaled layers.  For the layers of a low-bit model that stay out
+ * of 1 and 1.6 bits (the raw records of [BTE] ".tbin Format": first and last
+ * layers, LM head) and for layers of experts.  The pages name no such form; it
+ * is an interface of this library.
+ *
+ * Format.  Values are e4m3 bytes (1 sign, 4 exponent, 3 fraction bits, bias 7,
+ * largest 448, S.1111.111 = NaN, no infinity).  A packed row is
+ * kb = ceil(k/128) blocks of 128 bytes, back to back; bytes past k are 0 and
+ * are not masked by the matmuls.  Each block of 128 has a float32 scale:
+ *   activations  q uint8 [rows, 128 kb], scale float32 [kb, rows]: one scale
+ *                per row and block (the scales of a block's rows contiguous);
+ *   weights      q uint8 [n, 128 kb], scale float32 [ceil(n/128), kb]: one
+ *                scale per 128 x 128 block.  Experts are stacked:
+ *                q [groups, n, 128 kb], scale [groups, ceil(n/128), kb]; no
+ *                block crosses from one expert into the next.
+ * The value of a byte is e4m3(byte) * scale.  Packed buffers must be 16-byte
+ * aligned (BNN_ERR_MISALIGNED), scales 4-byte aligned.
+ *
+ * Sizes: rows, n, groups * n < 2^31, k <= BNN_MAX_K_FP8, groups <= BNN_MAX_GROUPS.
+ */
+#define BNN_MAX_K_FP8 (1 << 24)
+#define BNN_MAX_GROUPS 1024
+
+/* Element type of a float operand. */
+typedef enum { BNN_TYPE_F32 = 0, BNN_TYPE_BF16 = 1, BNN_TYPE_F16 = 2 } bnn_type;
+
+/*
+ * bnn_fp8_pack_rows -- pack activations: e4m3 rows with one scale per row and
+ * 128 elements of k, rows optionally picked by an index (the dispatch of tokens
+ * into expert order).
+ *
+ *   x       [x_rows, k] of x_type (a bnn_type), device, aligned to its element.
+ *   index   int32 [rows], device, or NULL.  Output row i is row index[i] of x
+ *           (row i without an index, and then x_rows >= rows).  An index
+ *           outside [0, x_rows) gives a row of zeros.
+ *   q       uint8 [rows, 128 kb], device, 16-byte aligned.
+ *   scale   float32 [kb, rows], device.
+ *   Per block, with a = max(max |x|, 2^-100):
+ *     scale = fl32(a / 448), r = fl32(448 / a), q = e4m3(fl32(x r)), rounded to
+ *     nearest even and saturated at 448.  So |e4m3(q) * scale - x| is at most
+ *     2^-4 |x| (half a step) plus a * 2^-18 (half the least step, 2^-10 of the
+ *     scale), times 1 + 2^-21 for the float32 roundings.
+ *   A block that holds an infinity or a NaN gets scale NaN and q = 0, so every
+ *   output that it enters is NaN.
+ */
+bnn_status bnn_fp8_pack_rows(const void* x, int x_type, int64_t x_rows, const int32_t* index, int64_t rows, int64_t k,
+                             uint8_t* q, float* scale, cudaStream_t s);
+
+/*
+ * bnn_fp8_pack_weight -- pack weights: e4m3 rows with one scale per 128 x 128
+ * block, for one matrix (groups = 1) or a stack of experts.
+ *
+ *   w       [groups, n, k] of w_type, device, aligned to its element.
+ *   q       uint8 [groups, n, 128 kb], device, 16-byte aligned.
+ *   scale   float32 [groups, ceil(n/128), kb], device.
+ *   The rule of bnn_fp8_pack_rows with the maximum over the block's 128 x 128
+ *   elements (fewer at the edges).
+ */
+bnn_status bnn_fp8_pack_weight(const void* w, int w_type, int64_t groups, int64_t n, int64_t k, uint8_t* q,
+                               float* scale, cudaStream_t s);
+
+/*
+ * bnn_fp8_gemm -- matrix product of packed activations and weights.
+ *
+ *   xq, xs  packed activations [m, 128 kb] and scales [kb, m], device.
+ *   wq, ws  packed weights [n, 128 kb] and scales [ceil(n/128), kb], device.
+ *   bias    float32 [n], device, or NULL.
+ *   out     [m, n] of out_type, device, aligned to its element:
+ *     out[i,j] = round(sum_b xs[b,i] ws[j/128,b] sum_{e in block b} xq[i,e] wq[j,e] + bias[j]).
+ *   The products are exact, each block's sum is taken in float32 by the tensor
+ *   cores, the blocks' sums are scaled and added in float32 in an order that
+ *   the sizes alone decide (results are bitwise reproducible), and there is one
+ *   rounding to out_type.  Finite results need xs * ws finite in float32.
+ *   wq and ws are weights in the sense of "Weights are static data" above.
+ */
+bnn_status bnn_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const float* bias,
+                        int64_t m, int64_t n, int64_t k, void* out, int out_type, cudaStream_t s);
+
+/*
+ * bnn_fp8_grouped_gemm -- matrix products grouped by expert with ragged sizes:
+ * the rows offsets[g] <= i < offsets[g+1] are multiplied with expert g's
+ * weights.  The sizes are read on the device: nothing is copied to the host,
+ * and a captured call follows the offsets of each replay.
+ *
+ *   xq, xs   packed activations [rows, 128 kb] and scales [kb, rows], device.
+ *   wq, ws   packed weights of all experts [groups, n, 128 kb] and scales
+ *            [groups, ceil(n/128), kb], device.
+ *   offsets  int64 [groups + 1], device, 8-byte aligned.  Groups may be empty.
+ *            Offsets are read as clamped to [0, rows] and to no less than the
+ *            largest before them, so that any contents stay inside the buffers.
+ *   out      [rows, n] of out_type, device: rows before offsets[0] and from
+ *            offsets[groups] on are left as they were.
+ *   Sums and rounding as for bnn_fp8_gemm; wq and ws are weights in the sense
+ *   of "Weights are static data" (the offsets are not).
+ */
+bnn_status bnn_fp8_grouped_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
+                                const int64_t* offsets, int64_t groups, int64_t rows, int64_t n, int64_t k, void* out,
+                                int out_type, cudaStream_t s);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* bnn_status_string(bnn_status st);

@@ -13,6 +13,7 @@ unsigned words travel in signed tensors of the same width, bit for bit):
   packed sign words   torch.int64  [rows, ceil(k/64)]   (uint64 in the ABI)
   base-3 trit words   torch.int16  [n, ceil(k/10)]      (uint16 in the ABI)
   bf16 activations    torch.bfloat16 [m, k]             (uint16 bit patterns in the ABI)
+  e4m3 rows           torch.float8_e4m3fn [rows, 128 ceil(k/128)]  (uint8 in the ABI)
 """
 from __future__ import annotations
 
@@ -44,6 +45,10 @@ _SIGS = {
     "bnn_ternary_sparse_count": [_vp, _i64, _i64, _vp, _vp],
     "bnn_ternary_sparse_encode": [_vp, _i64, _i64, _vp, _vp, _vp],
     "bnn_ternary_sparse_gemm": [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp],
+    "bnn_fp8_pack_rows": [_vp, _int, _i64, _vp, _i64, _i64, _vp, _vp, _vp],
+    "bnn_fp8_pack_weight": [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp],
+    "bnn_fp8_gemm": [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp],
+    "bnn_fp8_grouped_gemm": [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _int, _vp],
 }
 class TbinRecord(C.Structure):
     """bnn_tbin_record (include/bnn.h)."""
@@ -86,6 +91,9 @@ TERNARY_TWN, TERNARY_ABSMEAN, TERNARY_DELTA = 0, 1, 2
 TALGO_AUTO, TALGO_CUDA_CORES, TALGO_MMA, TALGO_TC = 0, 1, 2, 3
 MAX_K_BINARY = 1 << 24
 MAX_K_SPARSE = 1 << 15
+MAX_K_FP8 = 1 << 24
+MAX_GROUPS = 1024
+TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # bnn_type
 
 
 class BnnError(RuntimeError):
@@ -367,4 +375,155 @@ def bnn_ternary_linear(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tenso
     _dev(out, "out", torch.float32)
     _check(_lib.bnn_ternary_linear(_ptr(x), _ptr(packed), _ptr(scale), _ptr(bias), m, n, k, _ptr(out),
                                    _stream(x.device)), "bnn_ternary_linear")
+    return out
+
+
+def fp8_blocks(k: int) -> int:
+    """Blocks of 128 elements of an e4m3 row: the row holds 128 * fp8_blocks(k) bytes and as many scales."""
+    return (k + 127) // 128
+
+
+class _OnDevice:
+    """Makes the operands' device current for the library call (a no-op when it is already)."""
+
+    __slots__ = ("index", "before")
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the call on {device}")
+
+
+def _fp8_out(out, out_dtype, shape, device):
+    if out is None:
+        if out_dtype not in TYPES:
+            raise TypeError(f"out_dtype must be float32, bfloat16 or float16, got {out_dtype}")
+        return torch.empty(shape, dtype=out_dtype, device=device)
+    _dev(out, "out")
+    if out.dtype not in TYPES:
+        raise TypeError(f"out must be float32, bfloat16 or float16, got {out.dtype}")
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out must have shape {shape}, got {tuple(out.shape)}")
+    return out
+
+
+def _fp8_packed(q, scale, qshape, sshape, device):
+    if q is None:
+        q = torch.empty(qshape, dtype=torch.float8_e4m3fn, device=device)
+    if scale is None:
+        scale = torch.empty(sshape, dtype=torch.float32, device=device)
+    _dev(q, "q", torch.float8_e4m3fn, ndim=None)
+    _dev(scale, "scale", torch.float32, ndim=None)
+    if tuple(q.shape) != qshape or tuple(scale.shape) != sshape:
+        raise ValueError(f"q and scale must have shapes {qshape} and {sshape}")
+    return q, scale
+
+
+def bnn_fp8_pack_rows(x: torch.Tensor, index: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                      scale: torch.Tensor | None = None):
+    """float32/bfloat16/float16 [x_rows, k] -> (q float8_e4m3fn [rows, 128 kb], scale float32 [kb, rows]),
+    kb = ceil(k/128).  With an index (int32 [rows]) output row i is row index[i] of x (zeros where the
+    index is outside x)."""
+    _dev(x, "x")
+    if x.dtype not in TYPES:
+        raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
+    x_rows, k = x.shape
+    rows = x_rows
+    if index is not None:
+        _dev(index, "index", torch.int32, ndim=1)
+        rows = index.shape[0]
+    kb = fp8_blocks(k)
+    q, scale = _fp8_packed(q, scale, (rows, 128 * kb), (kb, rows), x.device)
+    _same_device(x.device, index=index, q=q, scale=scale)
+    with _OnDevice(x.device):
+        _check(_lib.bnn_fp8_pack_rows(_ptr(x), TYPES[x.dtype], x_rows, _ptr(index), rows, k, _ptr(q), _ptr(scale),
+                                      _stream(x.device)), "bnn_fp8_pack_rows")
+    return q, scale
+
+
+def bnn_fp8_pack_weight(w: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """float32/bfloat16/float16 [n, k] or [groups, n, k] -> (q float8_e4m3fn [.., n, 128 kb],
+    scale float32 [.., ceil(n/128), kb]): one scale per 128 x 128 block."""
+    _dev(w, "w", ndim=None)
+    if w.dtype not in TYPES:
+        raise TypeError(f"w must be float32, bfloat16 or float16, got {w.dtype}")
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w must be [n, k] or [groups, n, k], got shape {tuple(w.shape)}")
+    lead = tuple(w.shape[:-2])
+    n, k = w.shape[-2:]
+    groups = lead[0] if lead else 1
+    kb = fp8_blocks(k)
+    q, scale = _fp8_packed(q, scale, (*lead, n, 128 * kb), (*lead, fp8_blocks(n), kb), w.device)
+    _same_device(w.device, q=q, scale=scale)
+    with _OnDevice(w.device):
+        _check(_lib.bnn_fp8_pack_weight(_ptr(w), TYPES[w.dtype], groups, n, k, _ptr(q), _ptr(scale),
+                                        _stream(w.device)), "bnn_fp8_pack_weight")
+    return q, scale
+
+
+def _fp8_activations(xq, xs):
+    _dev(xq, "xq", torch.float8_e4m3fn)
+    _dev(xs, "xs", torch.float32)
+    m, kp = xq.shape
+    if kp % 128 or tuple(xs.shape) != (kp // 128, m):
+        raise ValueError("xq must be [m, 128 kb] and xs [kb, m]")
+    return m, kp
+
+
+def bnn_fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+                 bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """Packed activations [m, k] x packed weights [n, k] -> [m, n] in out_dtype (out's type when out is
+    given): scales applied, bias (float32 [n]) added."""
+    m, kp = _fp8_activations(xq, xs)
+    _dev(wq, "wq", torch.float8_e4m3fn)
+    _dev(ws, "ws", torch.float32)
+    n = wq.shape[0]
+    if wq.shape[1] != kp or tuple(ws.shape) != (fp8_blocks(n), kp // 128):
+        raise ValueError("wq must be [n, 128 kb] and ws [ceil(n/128), kb], with the kb of xq")
+    if bias is not None:
+        _dev(bias, "bias", torch.float32, ndim=1)
+        if bias.shape[0] != n:
+            raise ValueError("bias must have n elements")
+    out = _fp8_out(out, out_dtype, (m, n), xq.device)
+    _same_device(xq.device, xs=xs, wq=wq, ws=ws, bias=bias, out=out)
+    with _OnDevice(xq.device):
+        _check(_lib.bnn_fp8_gemm(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(bias), m, n, kp, _ptr(out),
+                                 TYPES[out.dtype], _stream(xq.device)), "bnn_fp8_gemm")
+    return out
+
+
+def bnn_fp8_grouped_gemm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+                         offsets: torch.Tensor, out_dtype: torch.dtype = torch.float32,
+                         out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows offsets[g] <= i < offsets[g+1] of the packed activations [rows, k] x expert g of the packed
+    weights [groups, n, k] -> [rows, n].  offsets int64 [groups + 1] stays on the device.  Rows outside
+    every group are left as they are in `out` (uninitialised when `out` is not given)."""
+    rows, kp = _fp8_activations(xq, xs)
+    _dev(wq, "wq", torch.float8_e4m3fn, ndim=3)
+    _dev(ws, "ws", torch.float32, ndim=3)
+    _dev(offsets, "offsets", torch.int64, ndim=1)
+    groups, n = wq.shape[0], wq.shape[1]
+    if wq.shape[2] != kp or tuple(ws.shape) != (groups, fp8_blocks(n), kp // 128):
+        raise ValueError("wq must be [groups, n, 128 kb] and ws [groups, ceil(n/128), kb], with the kb of xq")
+    if offsets.shape[0] != groups + 1:
+        raise ValueError("offsets must have groups + 1 elements")
+    out = _fp8_out(out, out_dtype, (rows, n), xq.device)
+    _same_device(xq.device, xs=xs, wq=wq, ws=ws, offsets=offsets, out=out)
+    with _OnDevice(xq.device):
+        _check(_lib.bnn_fp8_grouped_gemm(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(offsets), groups, rows, n, kp,
+                                         _ptr(out), TYPES[out.dtype], _stream(xq.device)), "bnn_fp8_grouped_gemm")
     return out
