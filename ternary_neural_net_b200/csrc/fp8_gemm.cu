@@ -3,98 +3,393 @@
 //
 //   y[i,j] = sum_b xs[b,i] ws[j/128,b] sum_{e in block b} xq[i,e] wq[j,e] (+ bias[j])
 //
-// First form: one thread per output, 16 x 16 outputs a CTA, both operands' tiles
-// of one block of k converted to float32 in shared memory.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
+// Both kernels (this file: few rows; fp8_gemm_pair.cu: many) run the inner sums
+// on tcgen05.mma kind::f8f6f4 (K = 32, four per block of 128) and start a fresh
+// accumulator for every block of k: the block's sum is read from tensor memory
+// and added, times its scales, to float32 accumulators in registers.  The
+// scales are arbitrary float32 numbers, so the tensor cores' own block scaling
+// (powers of two) cannot apply them.
+#include <cooperative_groups.h>
+#include <cstring>
 
-#include "bnn_internal.cuh"
+#include "fp8_common.cuh"
 
 namespace {
 
-constexpr int kTile = 16;
+using bnn::fp8::Args;
+using bnn::tc::mbar_arrive;
+using bnn::tc::mbar_expect_tx;
+using bnn::tc::mma_commit;
+using bnn::tc::smem_u32;
+using bnn::tc::sw128_desc;
+using bnn::tc::tma_load_2d;
+using bnn::tc::tmem_ld16;
+using bnn::tc::tmem_wait_ld;
 
-__device__ __forceinline__ float e4m3_value(uint8_t v) {
-  __nv_fp8_e4m3 t;
-  t.__x = v;
-  return static_cast<float>(t);
-}
+// ---------------------------------------------------------------------------
+// Few rows: weights on the tensor-memory lanes.
+//
+// Tile: 128 weight rows (one scale block: the weight scale of a block of k is
+// one number for the CTA) x BN activation rows as the MMA's N, so a handful of
+// rows costs a handful of columns and the weights stream once at whatever rate
+// HBM gives.  Stages of one block of k (128 bytes a row, one 128-byte-swizzled
+// TMA box per operand).  When the tiles leave SMs idle, a cluster of KS CTAs
+// splits the blocks of k and adds its partial sums in rank order through
+// distributed shared memory: the order is fixed, so results are reproducible.
+//
+// Roles: a TMA thread; an MMA thread; four epilogue warps, each 32 weight rows:
+// they read a block's BN sums (tcgen05.ld), scale and add them.  The scales of
+// the BN rows reach every lane through a per-warp line of shared memory, loaded
+// ahead from global memory (coalesced: the scale matrix is block-major).
+//
+// Launched with programmatic dependent launch: the weights' first stages are
+// fetched before the wait for the kernel ahead (not for groups, whose tiles
+// depend on the offsets).
+// ---------------------------------------------------------------------------
+constexpr int kTm = 128;                    // weight rows of a tile
+constexpr int kBlockBytes = 128;            // bytes of a row's block of k
+constexpr int kEpi = 128;                   // epilogue threads
+constexpr int kThreads = kEpi + 64;         // + TMA warp + MMA warp
+constexpr int kTmaWarp = kEpi / 32, kMmaWarp = kTmaWarp + 1;
+constexpr int kAhead = 4;                   // blocks whose activation scales are in flight
 
-__device__ __forceinline__ void store_out(void* out, int type, int64_t at, float y) {
-  if (type == BNN_TYPE_F32)
-    static_cast<float*>(out)[at] = y;
-  else if (type == BNN_TYPE_BF16)
-    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(y);
-  else
-    static_cast<__half*>(out)[at] = __float2half_rn(y);
-}
+template <int BN>
+struct Cfg {
+  static constexpr uint32_t kStageBytes = (kTm + BN) * kBlockBytes;
+  static constexpr int kStages = BN <= 32 ? 5 : (BN == 64 ? 4 : 3);  // two CTAs an SM (up to 113 KiB each)
+  static constexpr int kBufs = BN <= 16 ? 8 : (BN <= 64 ? 4 : 2);    // accumulators in tensor memory
+  static constexpr uint32_t kTmemCols = BN * kBufs;                  // 128 or 256: two CTAs fit the 512
+  static constexpr size_t kSmem = kStages * kStageBytes + 1024;
+};
+static_assert(Cfg<16>::kStageBytes % 1024 == 0 && Cfg<32>::kStageBytes % 1024 == 0, "swizzle atoms stay aligned");
 
-// offsets == nullptr: one group of all rows.
-__global__ void __launch_bounds__(kTile* kTile)
-fp8_gemm_simple_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
-                       const float* __restrict__ ws, const float* __restrict__ bias,
-                       const int64_t* __restrict__ offsets, int groups, int64_t rows, int64_t n, int64_t kb,
-                       void* __restrict__ out, int out_type) {
-  __shared__ float xt[kTile][129], wt[kTile][129];
-  const int tx = threadIdx.x % kTile, ty = threadIdx.x / kTile;
-  const int64_t nb = (n + 127) / 128;
-  for (int64_t tile = blockIdx.y; tile * kTile < rows + static_cast<int64_t>(groups) * kTile; tile += gridDim.y) {
-    // the tile's group: groups are cut into tiles of kTile rows one after another
-    int64_t i0 = tile * kTile, end = rows, g = 0;
-    if (offsets) {
-      int64_t left = tile, lo = 0;
-      bool found = false;
-      int64_t prev = max(int64_t{0}, min(rows, offsets[0]));
-      for (g = 0; g < groups; ++g) {
-        const int64_t next = max(prev, min(rows, offsets[g + 1]));
-        const int64_t tiles = (next - prev + kTile - 1) / kTile;
-        if (left < tiles) {
-          lo = prev + left * kTile;
-          end = next;
-          found = true;
-          break;
-        }
-        left -= tiles;
-        prev = next;
-      }
-      if (!found) return;
-      i0 = lo;
+template <int BN, int KS, bool GROUPED>
+__global__ void __launch_bounds__(kThreads, 2)
+fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                  const float* __restrict__ xs, const float* __restrict__ ws, const float* __restrict__ bias,
+                  const int64_t* __restrict__ offsets, int groups, int64_t rows, int64_t n, int kb,
+                  void* __restrict__ out, int out_type, unsigned int* errors) {
+  static_assert(KS == 1 || !GROUPED, "a split cluster takes one tile");
+  namespace cg = cooperative_groups;
+  using C = Cfg<BN>;
+  constexpr int S = C::kStages, NB = C::kBufs;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], part_full[NB], part_empty[NB];
+  __shared__ uint32_t tmem_holder;
+  __shared__ volatile int abort_flag;
+  __shared__ int any_bad;
+  __shared__ __align__(16) float scales[4][2][BN];
+  __shared__ bnn::fp8::Groups<GROUPED ? BNN_MAX_GROUPS : 1> map;
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = smem_u32(smem);
+  const int rank = KS > 1 ? static_cast<int>(blockIdx.x % KS) : 0;
+  const int wtiles = static_cast<int>((n + kTm - 1) / kTm);
+  const int b0 = static_cast<int>(static_cast<int64_t>(kb) * rank / KS);
+  const int b1 = static_cast<int>(static_cast<int64_t>(kb) * (rank + 1) / KS);
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      bnn::tc::mbar_init(smem_u32(&full_bar[i]), 1);
+      bnn::tc::mbar_init(smem_u32(&empty_bar[i]), 1);
     }
-    if (i0 >= end) return;
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    const int64_t i = i0 + ty, j = j0 + tx;
-    float acc = 0.0f;
-    for (int64_t b = 0; b < kb; ++b) {
-      __syncthreads();
-      for (int t = threadIdx.x; t < kTile * 128; t += kTile * kTile) {
-        const int r = t / 128, e = t % 128;
-        xt[r][e] = i0 + r < end ? e4m3_value(xq[(i0 + r) * kb * 128 + b * 128 + e]) : 0.0f;
-        wt[r][e] = j0 + r < n ? e4m3_value(wq[(g * n + j0 + r) * kb * 128 + b * 128 + e]) : 0.0f;
-      }
-      __syncthreads();
-      float part = 0.0f;
-      for (int e = 0; e < 128; ++e) part = fmaf(xt[ty][e], wt[tx][e], part);
-      if (i < end && j < n) acc = fmaf(part, xs[b * rows + i] * ws[(g * nb + j / 128) * kb + b], acc);
+    for (int i = 0; i < NB; ++i) {
+      bnn::tc::mbar_init(smem_u32(&part_full[i]), 1);
+      bnn::tc::mbar_init(smem_u32(&part_empty[i]), 4);
     }
-    if (i < end && j < n) store_out(out, out_type, i * n + j, bias ? acc + bias[j] : acc);
+    abort_flag = 0;
+    any_bad = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
+  if (tid == kTmaWarp * 32) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_x)) : "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&tmem_holder)),
+                 "r"(C::kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
+  }
+  if (GROUPED) {
+    bnn::pdl_wait();  // the offsets may come from the preceding kernel
+    if (warp == 0) bnn::fp8::build_groups<BN>(map, offsets, groups, rows, lane);
+  } else if (tid == 0) {
+    map.start[0] = 0;
+    map.start[1] = static_cast<int>(rows);
+    map.first[0] = 0;
+    map.first[1] = static_cast<int>((rows + BN - 1) / BN);
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+  const uint32_t tmem = tmem_holder;
+  bnn::pdl_trigger();
+  const int64_t tiles = static_cast<int64_t>(map.first[groups]) * wtiles;
+  const int64_t step = gridDim.x / KS, tile0 = blockIdx.x / KS;
+
+  if (warp == kTmaWarp) {
+    // ------------------------------------------------------------ TMA copies
+    if (lane == 0) {
+      uint32_t it = 0;  // stages issued
+      bool ok = true, waited = GROUPED;
+      for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+        const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map.start, map.first, wtiles);
+        const int wrow = t.group * static_cast<int>(n) + t.wtile * kTm;
+        int b = b0;
+        if (!waited) {  // the first stages' weights, then the wait, then their activations
+          const int ahead = min(S, b1 - b0);
+          for (int i = 0; i < ahead; ++i) {
+            mbar_expect_tx(smem_u32(&full_bar[i]), C::kStageBytes);
+            tma_load_2d(ring + i * C::kStageBytes, &tmap_w, (b0 + i) * kBlockBytes, wrow, smem_u32(&full_bar[i]));
+          }
+          bnn::pdl_wait();
+          for (int i = 0; i < ahead; ++i)
+            tma_load_2d(ring + i * C::kStageBytes + kTm * kBlockBytes, &tmap_x, (b0 + i) * kBlockBytes, t.row,
+                        smem_u32(&full_bar[i]));
+          b += ahead;
+          it = static_cast<uint32_t>(ahead);
+          waited = true;
+        }
+        for (; b < b1; ++b, ++it) {
+          const int st = static_cast<int>(it % S);
+          if (it >= static_cast<uint32_t>(S) &&
+              !bnn::tc::mbar_wait(smem_u32(&empty_bar[st]), (it / S + 1) & 1u, &abort_flag, errors)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = ring + st * C::kStageBytes, bar = smem_u32(&full_bar[st]);
+          mbar_expect_tx(bar, C::kStageBytes);
+          tma_load_2d(dst, &tmap_w, b * kBlockBytes, wrow, bar);
+          tma_load_2d(dst + kTm * kBlockBytes, &tmap_x, b * kBlockBytes, t.row, bar);
+        }
+      }
+      // the CTA must not retire with copies in flight
+      for (uint32_t c = it >= static_cast<uint32_t>(S) ? it - S : 0; c < it; ++c)
+        bnn::tc::mbar_drain(smem_u32(&full_bar[c % S]), (c / S) & 1u, errors);
+    }
+    if (KS > 1) {
+      __syncwarp();
+      cluster.sync();
+      cluster.sync();
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      constexpr uint32_t word = bnn::fp8::mma_word(kTm, BN);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+        for (int b = b0; b < b1; ++b, ++it) {
+          const int st = static_cast<int>(it % S), pb = static_cast<int>(it % NB);
+          ok = (it < static_cast<uint32_t>(NB) ||
+                bnn::tc::mbar_wait(smem_u32(&part_empty[pb]), (it / NB + 1) & 1u, &abort_flag, errors)) &&
+               bnn::tc::mbar_wait(smem_u32(&full_bar[st]), (it / S) & 1u, &abort_flag, errors);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+          const uint64_t ad = sw128_desc(ring + st * C::kStageBytes);
+          const uint64_t bd = sw128_desc(ring + st * C::kStageBytes + kTm * kBlockBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            asm volatile(
+                "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem + pb * BN),
+                "l"(ad + static_cast<uint64_t>(2 * kk)), "l"(bd + static_cast<uint64_t>(2 * kk)), "r"(word),
+                "r"(kk > 0 ? 1u : 0u));
+          mma_commit(smem_u32(&empty_bar[st]));
+          mma_commit(smem_u32(&part_full[pb]));
+        }
+      }
+      // every MMA issued has completed before the CTA's memory is given back
+      for (uint32_t c = it >= static_cast<uint32_t>(S) ? it - S : 0; c < it; ++c)
+        bnn::tc::mbar_drain(smem_u32(&empty_bar[c % S]), (c / S) & 1u, errors);
+    }
+    if (KS > 1) {
+      __syncwarp();
+      cluster.sync();
+      cluster.sync();
+    }
+  } else {
+    // ------------------------------------------------------------ scale and add
+    if (!GROUPED) bnn::pdl_wait();  // the activation scales may come from the preceding kernel
+    constexpr int PL = (BN + 31) / 32;  // rows' scales a lane loads per block
+    uint32_t it = 0;
+    bool ok = true;
+    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+    const int64_t nb = wtiles;
+    for (int64_t tile = tile0; tile < tiles; tile += step) {
+      const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map.start, map.first, wtiles);
+      const float* wsp = ws + (t.group * nb + t.wtile) * kb;
+      const int live = min(BN, t.end - t.row);
+      float acc[BN];
+#pragma unroll
+      for (int c = 0; c < BN; ++c) acc[c] = 0.0f;
+      float pre[kAhead][PL];  // xs * ws of the blocks ahead
+      auto load = [&](int b, float (&v)[PL]) {
+        const float w = b < b1 ? __ldg(wsp + b) : 0.0f;
+#pragma unroll
+        for (int p = 0; p < PL; ++p) {
+          const int c = lane + 32 * p;
+          v[p] = b < b1 && c < live ? w * __ldg(xs + b * rows + t.row + c) : 0.0f;
+        }
+      };
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) load(b0 + a, pre[a]);
+      for (int b = b0; b < b1 && ok; b += kAhead) {
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          if (b + a < b1 && ok) {
+            float* line = scales[warp][a & 1];
+#pragma unroll
+            for (int p = 0; p < PL; ++p)
+              if (lane + 32 * p < BN) line[lane + 32 * p] = pre[a][p];
+            load(b + a + kAhead, pre[a]);
+            const int pb = static_cast<int>(it % NB);
+            ok = bnn::tc::mbar_wait(smem_u32(&part_full[pb]), (it / NB) & 1u, &abort_flag, errors);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+              asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+#pragma unroll
+              for (int c0 = 0; c0 < BN; c0 += 16) {
+                uint32_t r[16];
+                tmem_ld16(tmem + lanes + pb * BN + c0, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 16; c += 4) {
+                  const float4 s = *reinterpret_cast<const float4*>(line + c0 + c);
+                  acc[c0 + c] = fmaf(__uint_as_float(r[c]), s.x, acc[c0 + c]);
+                  acc[c0 + c + 1] = fmaf(__uint_as_float(r[c + 1]), s.y, acc[c0 + c + 1]);
+                  acc[c0 + c + 2] = fmaf(__uint_as_float(r[c + 2]), s.z, acc[c0 + c + 2]);
+                  acc[c0 + c + 3] = fmaf(__uint_as_float(r[c + 3]), s.w, acc[c0 + c + 3]);
+                }
+              }
+              asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+              __syncwarp();  // also orders this block's reads of `line` before its next writes
+              if (lane == 0) mbar_arrive(smem_u32(&part_empty[pb]));
+            }
+            ++it;
+          }
+        }
+      }
+      const int64_t j = static_cast<int64_t>(t.wtile) * kTm + tid;
+      const float bj = bias && j < n ? __ldg(bias + j) : 0.0f;
+      if (KS == 1) {
+        if (!ok) break;
+        if (j < n) {
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (c < live) bnn::fp8::store_one(out, out_type, (t.row + c) * n + j, acc[c] + bj);
+        }
+      } else {
+        // the cluster's sums: rank r adds columns [r BN / KS, (r + 1) BN / KS) of all ranks, in rank order
+        constexpr int kCols = BN / KS;
+        float* recv = reinterpret_cast<float*>(smem);
+        cluster.sync();  // every CTA's tensor core is done with its stages
+        if (!ok && lane == 0)
+          for (int q = 0; q < KS; ++q) atomicExch(cluster.map_shared_rank(&any_bad, q), 1);
+#pragma unroll
+        for (int c = 0; c < BN; ++c)
+          cluster.map_shared_rank(recv, c / kCols)[(rank * kCols + c % kCols) * kEpi + tid] = acc[c];
+        cluster.sync();  // every share has landed
+        if (j < n && !any_bad) {
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            float y = 0.0f;
+#pragma unroll
+            for (int q = 0; q < KS; ++q) y += recv[(q * kCols + c) * kEpi + tid];
+            if (rank * kCols + c < live)
+              bnn::fp8::store_one(out, out_type, (t.row + rank * kCols + c) * n + j, y + bj);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+  __syncthreads();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::kTmemCols));
 }
 
-bnn_status launch_simple(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const float* bias,
-                         const int64_t* offsets, int64_t groups, int64_t rows, int64_t n, int64_t kb, void* out,
-                         int out_type, cudaStream_t s) {
-  const int64_t gx = (n + kTile - 1) / kTile, gy = (rows + kTile - 1) / kTile + groups;
-  if (gx > INT32_MAX) return BNN_ERR_INVALID_ARG;
-  fp8_gemm_simple_kernel<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535)),
-                           kTile * kTile, 0, s>>>(xq, xs, wq, ws, bias, offsets, static_cast<int>(groups), rows, n, kb,
-                                                  out, out_type);
+// k = 0: every sum is empty.
+__global__ void fp8_empty_kernel(const float* __restrict__ bias, const int64_t* __restrict__ offsets, int groups,
+                                 int64_t rows, int64_t n, void* __restrict__ out, int out_type) {
+  int64_t lo = 0, hi = rows;
+  if (offsets) {
+    lo = max(int64_t{0}, min(rows, offsets[0]));
+    hi = lo;
+    for (int g = 1; g <= groups; ++g) hi = max(hi, min(rows, offsets[g]));
+  }
+  for (int64_t i = lo * n + blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < hi * n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    bnn::fp8::store_one(out, out_type, i, bias ? bias[i % n] : 0.0f);
+}
+
+bnn_status gemm_empty(const Args& a) {
+  fp8_empty_kernel<<<2 * bnn::sm_count(), 256, 0, a.stream>>>(a.bias, a.offsets, a.groups, a.rows, a.n, a.out,
+                                                              a.out_type);
   return bnn::check_launch();
 }
 
-size_t type_size(int type) { return type == BNN_TYPE_F32 ? 4 : 2; }
+template <int BN, int KS, bool GROUPED>
+bnn_status launch_narrow(const Args& a) {
+  const int64_t wtiles = (a.n + kTm - 1) / kTm;
+  // groups: at most one ragged tile each beside the full ones
+  const int64_t rtiles = GROUPED ? a.rows / BN + (a.rows < a.groups ? a.rows : a.groups) : (a.rows + BN - 1) / BN;
+  const int64_t tiles = rtiles * wtiles, slots = 2 * bnn::sm_count();
+  const int64_t ctas = KS > 1 ? tiles * KS : (tiles < slots ? tiles : slots);
+  // grid limits, and stages counted in 32 bits
+  if (ctas > INT32_MAX || (tiles + slots - 1) / slots * a.kb >= (int64_t{1} << 31)) return BNN_ERR_INVALID_ARG;
+  CUtensorMap tw, tx;
+  const uint64_t pitch = static_cast<uint64_t>(a.kb) * kBlockBytes;
+  if (!bnn::encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq, pitch, static_cast<uint64_t>(a.groups * a.n),
+                           pitch, kBlockBytes, kTm, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !bnn::encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.xq, pitch, static_cast<uint64_t>(a.rows), pitch,
+                           kBlockBytes, BN, CU_TENSOR_MAP_SWIZZLE_128B))
+    return BNN_ERR_UNSUPPORTED;
+  unsigned int* errors = bnn::device_error_counter();
+  if (!errors) return bnn::cuda_fail(cudaGetLastError());
+  auto kern = fp8_narrow_kernel<BN, KS, GROUPED>;
+  BNN_TRY(bnn::ensure_smem(kern, Cfg<BN>::kSmem));
+  const cudaError_t e =
+      bnn::launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Cfg<BN>::kSmem, a.stream, KS, tw, tx,
+                      a.xs, a.ws, a.bias, a.offsets, a.groups, a.rows, a.n, a.kb, a.out, a.out_type, errors);
+  if (e != cudaSuccess) return bnn::cuda_fail(e);
+  return bnn::check_launch();
+}
+
+template <int BN>
+bnn_status narrow(const Args& a) {
+  if (a.offsets) return launch_narrow<BN, 1, true>(a);
+  const int64_t tiles = (a.n + kTm - 1) / kTm * ((a.rows + BN - 1) / BN), slots = 2 * bnn::sm_count();
+  if (tiles * 8 <= slots && a.kb >= 16) return launch_narrow<BN, 8, false>(a);
+  if (tiles * 4 <= slots && a.kb >= 8) return launch_narrow<BN, 4, false>(a);
+  if (tiles * 2 <= slots && a.kb >= 4) return launch_narrow<BN, 2, false>(a);
+  return launch_narrow<BN, 1, false>(a);
+}
+
+bnn_status dispatch(const Args& a) {
+  if (a.kb == 0) return gemm_empty(a);
+  const int64_t per = a.offsets ? (a.rows + a.groups - 1) / a.groups : a.rows;
+  if (per > 128) return bnn::fp8::gemm_pair(a);
+  return bnn::fp8::gemm_narrow(a);
+}
 
 }  // namespace
+
+namespace bnn {
+namespace fp8 {
+
+bnn_status gemm_narrow(const Args& a) {
+  const int64_t per = a.offsets ? (a.rows + a.groups - 1) / a.groups : a.rows;
+  if (per <= 16) return narrow<16>(a);
+  if (per <= 32) return narrow<32>(a);
+  if (per <= 64) return narrow<64>(a);
+  return narrow<128>(a);
+}
+
+}  // namespace fp8
+}  // namespace bnn
 
 extern "C" bnn_status bnn_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                                    const float* bias, int64_t m, int64_t n, int64_t k, void* out, int out_type,
@@ -105,9 +400,9 @@ extern "C" bnn_status bnn_fp8_gemm(const uint8_t* xq, const float* xs, const uin
   if (m == 0 || n == 0) return BNN_OK;
   if (!out || (k > 0 && (!xq || !xs || !wq || !ws))) return BNN_ERR_INVALID_ARG;
   if (!bnn::aligned(xq, 16) || !bnn::aligned(wq, 16) || !bnn::aligned(xs, 4) || !bnn::aligned(ws, 4) ||
-      !bnn::aligned(bias, 4) || !bnn::aligned(out, type_size(out_type)))
+      !bnn::aligned(bias, 4) || !bnn::aligned(out, bnn::fp8::type_size(out_type)))
     return BNN_ERR_MISALIGNED;
-  return launch_simple(xq, xs, wq, ws, bias, nullptr, 1, m, n, (k + 127) / 128, out, out_type, s);
+  return dispatch(Args{xq, xs, wq, ws, bias, nullptr, 1, m, n, static_cast<int>((k + 127) / 128), out, out_type, s});
 }
 
 extern "C" bnn_status bnn_fp8_grouped_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
@@ -119,7 +414,8 @@ extern "C" bnn_status bnn_fp8_grouped_gemm(const uint8_t* xq, const float* xs, c
   if (groups == 0 || rows == 0 || n == 0) return BNN_OK;
   if (!out || !offsets || (k > 0 && (!xq || !xs || !wq || !ws))) return BNN_ERR_INVALID_ARG;
   if (!bnn::aligned(xq, 16) || !bnn::aligned(wq, 16) || !bnn::aligned(xs, 4) || !bnn::aligned(ws, 4) ||
-      !bnn::aligned(offsets, 8) || !bnn::aligned(out, type_size(out_type)))
+      !bnn::aligned(offsets, 8) || !bnn::aligned(out, bnn::fp8::type_size(out_type)))
     return BNN_ERR_MISALIGNED;
-  return launch_simple(xq, xs, wq, ws, nullptr, offsets, groups, rows, n, (k + 127) / 128, out, out_type, s);
+  return dispatch(Args{xq, xs, wq, ws, nullptr, offsets, static_cast<int>(groups), rows, n,
+                       static_cast<int>((k + 127) / 128), out, out_type, s});
 }
