@@ -383,28 +383,26 @@ def fp8_blocks(k: int) -> int:
     return (k + 127) // 128
 
 
-class _OnDevice:
-    """Makes the operands' device current for the library call (a no-op when it is already)."""
-
-    __slots__ = ("index", "before")
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _fp8_call(name, call, device, *args):
+    """call(*args, stream) with the operands' device current; tensors go as their pointers, None as NULL.
+    (A decoding step makes hundreds of these calls, each of a few microseconds on the GPU.)"""
+    index = device.index
+    before = torch.cuda.current_device()
+    if before != index:
+        torch.cuda.set_device(index)
+    try:
+        st = call(*args, torch.cuda.current_stream(index).cuda_stream)
+    finally:
+        if before != index:
+            torch.cuda.set_device(before)
+    if st != BNN_OK:
+        raise BnnError(st, name)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
+def _same_device(device, *tensors):
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the call on {device}")
+            raise ValueError(f"operands are on {t.device} and {device}")
 
 
 def _fp8_out(out, out_dtype, shape, device):
@@ -423,11 +421,13 @@ def _fp8_out(out, out_dtype, shape, device):
 def _fp8_packed(q, scale, qshape, sshape, device):
     if q is None:
         q = torch.empty(qshape, dtype=torch.float8_e4m3fn, device=device)
+    else:
+        _dev(q, "q", torch.float8_e4m3fn, ndim=None)
     if scale is None:
         scale = torch.empty(sshape, dtype=torch.float32, device=device)
-    _dev(q, "q", torch.float8_e4m3fn, ndim=None)
-    _dev(scale, "scale", torch.float32, ndim=None)
-    if tuple(q.shape) != qshape or tuple(scale.shape) != sshape:
+    else:
+        _dev(scale, "scale", torch.float32, ndim=None)
+    if q.shape != qshape or scale.shape != sshape:
         raise ValueError(f"q and scale must have shapes {qshape} and {sshape}")
     return q, scale
 
@@ -447,10 +447,9 @@ def bnn_fp8_pack_rows(x: torch.Tensor, index: torch.Tensor | None = None, q: tor
         rows = index.shape[0]
     kb = fp8_blocks(k)
     q, scale = _fp8_packed(q, scale, (rows, 128 * kb), (kb, rows), x.device)
-    _same_device(x.device, index=index, q=q, scale=scale)
-    with _OnDevice(x.device):
-        _check(_lib.bnn_fp8_pack_rows(_ptr(x), TYPES[x.dtype], x_rows, _ptr(index), rows, k, _ptr(q), _ptr(scale),
-                                      _stream(x.device)), "bnn_fp8_pack_rows")
+    _same_device(x.device, index, q, scale)
+    _fp8_call("bnn_fp8_pack_rows", _lib.bnn_fp8_pack_rows, x.device, x.data_ptr(), TYPES[x.dtype], x_rows,
+              None if index is None else index.data_ptr(), rows, k, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -467,10 +466,9 @@ def bnn_fp8_pack_weight(w: torch.Tensor, q: torch.Tensor | None = None, scale: t
     groups = lead[0] if lead else 1
     kb = fp8_blocks(k)
     q, scale = _fp8_packed(q, scale, (*lead, n, 128 * kb), (*lead, fp8_blocks(n), kb), w.device)
-    _same_device(w.device, q=q, scale=scale)
-    with _OnDevice(w.device):
-        _check(_lib.bnn_fp8_pack_weight(_ptr(w), TYPES[w.dtype], groups, n, k, _ptr(q), _ptr(scale),
-                                        _stream(w.device)), "bnn_fp8_pack_weight")
+    _same_device(w.device, q, scale)
+    _fp8_call("bnn_fp8_pack_weight", _lib.bnn_fp8_pack_weight, w.device, w.data_ptr(), TYPES[w.dtype], groups, n, k,
+              q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -478,7 +476,7 @@ def _fp8_activations(xq, xs):
     _dev(xq, "xq", torch.float8_e4m3fn)
     _dev(xs, "xs", torch.float32)
     m, kp = xq.shape
-    if kp % 128 or tuple(xs.shape) != (kp // 128, m):
+    if kp % 128 or xs.shape != (kp // 128, m):
         raise ValueError("xq must be [m, 128 kb] and xs [kb, m]")
     return m, kp
 
@@ -492,17 +490,16 @@ def bnn_fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch
     _dev(wq, "wq", torch.float8_e4m3fn)
     _dev(ws, "ws", torch.float32)
     n = wq.shape[0]
-    if wq.shape[1] != kp or tuple(ws.shape) != (fp8_blocks(n), kp // 128):
+    if wq.shape[1] != kp or ws.shape != (fp8_blocks(n), kp // 128):
         raise ValueError("wq must be [n, 128 kb] and ws [ceil(n/128), kb], with the kb of xq")
     if bias is not None:
         _dev(bias, "bias", torch.float32, ndim=1)
         if bias.shape[0] != n:
             raise ValueError("bias must have n elements")
     out = _fp8_out(out, out_dtype, (m, n), xq.device)
-    _same_device(xq.device, xs=xs, wq=wq, ws=ws, bias=bias, out=out)
-    with _OnDevice(xq.device):
-        _check(_lib.bnn_fp8_gemm(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(bias), m, n, kp, _ptr(out),
-                                 TYPES[out.dtype], _stream(xq.device)), "bnn_fp8_gemm")
+    _same_device(xq.device, xs, wq, ws, bias, out)
+    _fp8_call("bnn_fp8_gemm", _lib.bnn_fp8_gemm, xq.device, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+              None if bias is None else bias.data_ptr(), m, n, kp, out.data_ptr(), TYPES[out.dtype])
     return out
 
 
@@ -517,13 +514,12 @@ def bnn_fp8_grouped_gemm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, w
     _dev(ws, "ws", torch.float32, ndim=3)
     _dev(offsets, "offsets", torch.int64, ndim=1)
     groups, n = wq.shape[0], wq.shape[1]
-    if wq.shape[2] != kp or tuple(ws.shape) != (groups, fp8_blocks(n), kp // 128):
+    if wq.shape[2] != kp or ws.shape != (groups, fp8_blocks(n), kp // 128):
         raise ValueError("wq must be [groups, n, 128 kb] and ws [groups, ceil(n/128), kb], with the kb of xq")
     if offsets.shape[0] != groups + 1:
         raise ValueError("offsets must have groups + 1 elements")
     out = _fp8_out(out, out_dtype, (rows, n), xq.device)
-    _same_device(xq.device, xs=xs, wq=wq, ws=ws, offsets=offsets, out=out)
-    with _OnDevice(xq.device):
-        _check(_lib.bnn_fp8_grouped_gemm(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(offsets), groups, rows, n, kp,
-                                         _ptr(out), TYPES[out.dtype], _stream(xq.device)), "bnn_fp8_grouped_gemm")
+    _same_device(xq.device, xs, wq, ws, offsets, out)
+    _fp8_call("bnn_fp8_grouped_gemm", _lib.bnn_fp8_grouped_gemm, xq.device, xq.data_ptr(), xs.data_ptr(),
+              wq.data_ptr(), ws.data_ptr(), offsets.data_ptr(), groups, rows, n, kp, out.data_ptr(), TYPES[out.dtype])
     return out

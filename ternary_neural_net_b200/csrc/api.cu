@@ -125,8 +125,8 @@ EncodeTiled g_encode = nullptr;
 std::once_flag g_encode_once;
 }  // namespace
 
-bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows,
-                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+namespace {
+bool load_encoder() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -134,13 +134,31 @@ bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base
         q == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<EncodeTiled>(fn);
   });
-  if (!g_encode || inner == 0 || rows == 0) return false;
+  return g_encode != nullptr;
+}
+}  // namespace
+
+bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows,
+                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  if (!load_encoder() || inner == 0 || rows == 0) return false;
   const cuuint64_t dims[2] = {inner, rows};
   const cuuint64_t strides[1] = {row_bytes};
   const cuuint32_t box[2] = {box_inner, box_rows};
   const cuuint32_t estride[2] = {1, 1};
   return g_encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tmap_blocks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t kb, uint32_t box_rows,
+                        uint32_t box_blocks) {
+  if (!load_encoder() || rows == 0 || kb == 0) return false;
+  const cuuint64_t dims[3] = {128, rows, kb};
+  const cuuint64_t strides[2] = {kb * 128, 128};
+  const cuuint32_t box[3] = {128, box_rows, box_blocks};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estride,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int current_device() {

@@ -59,6 +59,12 @@ cudaError_t ensure_smem(Kernel kern, size_t bytes) {
 bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows,
                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
+// The 3-D TMA descriptor of packed e4m3 rows (rows of kb blocks of 128 bytes,
+// back to back): boxes of 128 bytes x box_rows rows x box_blocks blocks of k,
+// 128-byte swizzled; rows and blocks outside the matrix read as zero.
+bool encode_tmap_blocks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t kb, uint32_t box_rows,
+                        uint32_t box_blocks);
+
 // Programmatic dependent launch.  A kernel launched with launch_pdl may start
 // while the preceding kernel on the stream is still running; it must call
 // pdl_wait() before it reads anything that kernel writes and before its own

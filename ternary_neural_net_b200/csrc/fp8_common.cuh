@@ -27,8 +27,81 @@ struct Args {
   cudaStream_t stream;
 };
 
-bnn_status gemm_narrow(const Args& a);
-bnn_status gemm_pair(const Args& a);
+// Up to 8 rows, one group.
+bnn_status gemm_skinny(const Args& a);
+// Tiles of 128 (ctas = 1) or 256 rows (a CTA pair) x tn columns.
+bnn_status gemm_tile(const Args& a, int ctas, int tn);
+
+// Bounded wait for an mbarrier phase: up to kPolls polls in a loop of four
+// instructions.  (bnn::tc::mbar_wait bounds by the wall clock; its code around
+// every wait costs these kernels, which wait twice per block of k and role, more
+// than the waits themselves; and polls with a time hint wake hundreds of clocks
+// late.)  Every thread has waited for the kernel ahead before its first call, so
+// only copies and MMAs of this kernel are waited for: microseconds, against
+// 10 ms of polls at the least.  False when it ran out: counted in *errors by
+// each thread.
+constexpr uint32_t kPolls = 1u << 20;
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, unsigned int* errors) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p, q;\n.reg .u32 i;\nmov.u32 i, 0;\n"
+      "POLL:\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n@p bra DONE;\n"
+      "add.u32 i, i, 1;\nsetp.lt.u32 q, i, %3;\n@q bra POLL;\n"
+      "DONE:\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "n"(kPolls)
+      : "memory");
+  if (!ok) atomicAdd(errors, 1u);
+  return ok != 0;
+}
+
+// The same for two barriers at once: the polls' latencies overlap.
+__device__ __forceinline__ bool wait2(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b,
+                                      unsigned int* errors) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p, q;\n.reg .u32 i;\nmov.u32 i, 0;\n"
+      "POLL:\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\nand.pred p, p, q;\n@p bra DONE;\n"
+      "add.u32 i, i, 1;\nsetp.lt.u32 q, i, %5;\n@q bra POLL;\n"
+      "DONE:\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar_a), "r"(parity_a), "r"(bar_b), "r"(parity_b), "n"(kPolls)
+      : "memory");
+  if (!ok) atomicAdd(errors, 1u);
+  return ok != 0;
+}
+
+// Position in a ring of N slots and the parity of its current round.
+template <int N>
+struct Ring {
+  uint32_t at = 0, round = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      round ^= 1u;
+    }
+  }
+};
+
+// True in one thread of a converged warp (the same one each time).  The copy and
+// MMA warps run their loops as whole warps and issue inside if (elected()): a
+// loop that one lane runs by itself takes several times as long per wait and
+// per issue, since these instructions take warp-uniform operands.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
+// Arrival on an mbarrier of the cluster (a shared::cluster address) without
+// memory ordering: what it orders is tensor memory, which the tcgen05 fences
+// around it and around the wait cover.  (With release at cluster scope it would
+// first wait for every load in flight: the scales fetched ahead.)
+__device__ __forceinline__ void arrive_cluster(uint32_t remote) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(remote) : "memory");
+}
 
 // Instruction word of tcgen05.mma kind::f8f6f4: float32 accumulator, both
 // operands e4m3 and K-major, an m x n tile.
@@ -116,6 +189,28 @@ __device__ __forceinline__ void store_one(void* out, int type, int64_t at, float
     static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(y);
   else
     static_cast<__half*>(out)[at] = __float2half_rn(y);
+}
+
+// Eight consecutive outputs at a 16-byte aligned place.
+__device__ __forceinline__ void store_eight(void* out, int type, int64_t at, const float (&y)[8]) {
+  if (type == BNN_TYPE_F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+    p[0] = make_float4(y[0], y[1], y[2], y[3]);
+    p[1] = make_float4(y[4], y[5], y[6], y[7]);
+    return;
+  }
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (type == BNN_TYPE_BF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+      v[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+      v[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 inline size_t type_size(int type) { return type == BNN_TYPE_F32 ? 4 : 2; }

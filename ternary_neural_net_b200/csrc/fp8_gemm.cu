@@ -3,14 +3,13 @@
 //
 //   y[i,j] = sum_b xs[b,i] ws[j/128,b] sum_{e in block b} xq[i,e] wq[j,e] (+ bias[j])
 //
-// Both kernels (this file: few rows; fp8_gemm_pair.cu: many) run the inner sums
+// Both kernels (this file: few rows; fp8_gemm_tile.cu: more) run the inner sums
 // on tcgen05.mma kind::f8f6f4 (K = 32, four per block of 128) and start a fresh
 // accumulator for every block of k: the block's sum is read from tensor memory
 // and added, times its scales, to float32 accumulators in registers.  The
 // scales are arbitrary float32 numbers, so the tensor cores' own block scaling
 // (powers of two) cannot apply them.
 #include <cooperative_groups.h>
-#include <cstring>
 
 #include "fp8_common.cuh"
 
@@ -56,9 +55,9 @@ constexpr int kAhead = 4;                   // blocks whose activation scales ar
 template <int BN>
 struct Cfg {
   static constexpr uint32_t kStageBytes = (kTm + BN) * kBlockBytes;
-  static constexpr int kStages = BN <= 32 ? 5 : (BN == 64 ? 4 : 3);  // two CTAs an SM (up to 113 KiB each)
-  static constexpr int kBufs = BN <= 16 ? 8 : (BN <= 64 ? 4 : 2);    // accumulators in tensor memory
-  static constexpr uint32_t kTmemCols = BN * kBufs;                  // 128 or 256: two CTAs fit the 512
+  static constexpr int kStages = 5;                                  // two CTAs an SM (up to 113 KiB each)
+  static constexpr int kBufs = 128 / BN;                               // accumulators in tensor memory
+  static constexpr uint32_t kTmemCols = BN * kBufs;                  // 128: two CTAs (and the next kernel's) fit the 512
   static constexpr size_t kSmem = kStages * kStageBytes + 1024;
 };
 static_assert(Cfg<16>::kStageBytes % 1024 == 0 && Cfg<32>::kStageBytes % 1024 == 0, "swizzle atoms stay aligned");
@@ -76,7 +75,6 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], part_full[NB], part_empty[NB];
   __shared__ uint32_t tmem_holder;
-  __shared__ volatile int abort_flag;
   __shared__ int any_bad;
   __shared__ __align__(16) float scales[4][2][BN];
   __shared__ bnn::fp8::Groups<GROUPED ? BNN_MAX_GROUPS : 1> map;
@@ -98,7 +96,6 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
       bnn::tc::mbar_init(smem_u32(&part_full[i]), 1);
       bnn::tc::mbar_init(smem_u32(&part_empty[i]), 4);
     }
-    abort_flag = 0;
     any_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -130,44 +127,50 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ TMA copies
-    if (lane == 0) {
-      uint32_t it = 0;  // stages issued
-      bool ok = true, waited = GROUPED;
-      for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
-        const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map.start, map.first, wtiles);
-        const int wrow = t.group * static_cast<int>(n) + t.wtile * kTm;
-        int b = b0;
-        if (!waited) {  // the first stages' weights, then the wait, then their activations
-          const int ahead = min(S, b1 - b0);
-          for (int i = 0; i < ahead; ++i) {
+    uint32_t it = 0;  // stages issued
+    bool ok = true, waited = GROUPED;
+    for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+      const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map.start, map.first, wtiles);
+      const int wrow = t.group * static_cast<int>(n) + t.wtile * kTm;
+      int b = b0;
+      if (!waited) {  // the first stages' weights, then the wait, then their activations
+        const int ahead = min(S, b1 - b0);
+        for (int i = 0; i < ahead; ++i) {
+          if (bnn::fp8::elected()) {
             mbar_expect_tx(smem_u32(&full_bar[i]), C::kStageBytes);
             tma_load_2d(ring + i * C::kStageBytes, &tmap_w, (b0 + i) * kBlockBytes, wrow, smem_u32(&full_bar[i]));
           }
-          bnn::pdl_wait();
-          for (int i = 0; i < ahead; ++i)
+          __syncwarp();
+        }
+        bnn::pdl_wait();
+        for (int i = 0; i < ahead; ++i) {
+          if (bnn::fp8::elected())
             tma_load_2d(ring + i * C::kStageBytes + kTm * kBlockBytes, &tmap_x, (b0 + i) * kBlockBytes, t.row,
                         smem_u32(&full_bar[i]));
-          b += ahead;
-          it = static_cast<uint32_t>(ahead);
-          waited = true;
+          __syncwarp();
         }
-        for (; b < b1; ++b, ++it) {
-          const int st = static_cast<int>(it % S);
-          if (it >= static_cast<uint32_t>(S) &&
-              !bnn::tc::mbar_wait(smem_u32(&empty_bar[st]), (it / S + 1) & 1u, &abort_flag, errors)) {
-            ok = false;
-            break;
-          }
+        b += ahead;
+        it = static_cast<uint32_t>(ahead);
+        waited = true;
+      }
+      for (; b < b1; ++b, ++it) {
+        const int st = static_cast<int>(it % S);
+        if (it >= static_cast<uint32_t>(S))
+          ok = bnn::fp8::wait(smem_u32(&empty_bar[st]), (it / S + 1) & 1u, errors);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (bnn::fp8::elected()) {
           const uint32_t dst = ring + st * C::kStageBytes, bar = smem_u32(&full_bar[st]);
           mbar_expect_tx(bar, C::kStageBytes);
           tma_load_2d(dst, &tmap_w, b * kBlockBytes, wrow, bar);
           tma_load_2d(dst + kTm * kBlockBytes, &tmap_x, b * kBlockBytes, t.row, bar);
         }
+        __syncwarp();
       }
-      // the CTA must not retire with copies in flight
-      for (uint32_t c = it >= static_cast<uint32_t>(S) ? it - S : 0; c < it; ++c)
-        bnn::tc::mbar_drain(smem_u32(&full_bar[c % S]), (c / S) & 1u, errors);
     }
+    // the CTA must not retire with copies in flight
+    for (uint32_t c = it >= static_cast<uint32_t>(S) ? it - S : 0; c < it; ++c)
+      bnn::tc::mbar_drain(smem_u32(&full_bar[c % S]), (c / S) & 1u, errors);
     if (KS > 1) {
       __syncwarp();
       cluster.sync();
@@ -175,18 +178,20 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      constexpr uint32_t word = bnn::fp8::mma_word(kTm, BN);
-      uint32_t it = 0;
-      bool ok = true;
-      for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
-        for (int b = b0; b < b1; ++b, ++it) {
-          const int st = static_cast<int>(it % S), pb = static_cast<int>(it % NB);
-          ok = (it < static_cast<uint32_t>(NB) ||
-                bnn::tc::mbar_wait(smem_u32(&part_empty[pb]), (it / NB + 1) & 1u, &abort_flag, errors)) &&
-               bnn::tc::mbar_wait(smem_u32(&full_bar[st]), (it / S) & 1u, &abort_flag, errors);
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+    if (!GROUPED) bnn::pdl_wait();  // before the first bounded wait (for copies that start after it)
+    constexpr uint32_t word = bnn::fp8::mma_word(kTm, BN);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+      for (int b = b0; b < b1; ++b, ++it) {
+        const int st = static_cast<int>(it % S), pb = static_cast<int>(it % NB);
+        if (it >= static_cast<uint32_t>(NB))
+          ok = bnn::fp8::wait(smem_u32(&part_empty[pb]), (it / NB + 1) & 1u, errors);
+        if (ok) ok = bnn::fp8::wait(smem_u32(&full_bar[st]), (it / S) & 1u, errors);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+        if (bnn::fp8::elected()) {
           const uint64_t ad = sw128_desc(ring + st * C::kStageBytes);
           const uint64_t bd = sw128_desc(ring + st * C::kStageBytes + kTm * kBlockBytes);
 #pragma unroll
@@ -199,11 +204,12 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
           mma_commit(smem_u32(&empty_bar[st]));
           mma_commit(smem_u32(&part_full[pb]));
         }
+        __syncwarp();
       }
-      // every MMA issued has completed before the CTA's memory is given back
-      for (uint32_t c = it >= static_cast<uint32_t>(S) ? it - S : 0; c < it; ++c)
-        bnn::tc::mbar_drain(smem_u32(&empty_bar[c % S]), (c / S) & 1u, errors);
     }
+    // every MMA issued has completed before the CTA's memory is given back
+    for (uint32_t c = it >= static_cast<uint32_t>(S) ? it - S : 0; c < it; ++c)
+      bnn::tc::mbar_drain(smem_u32(&empty_bar[c % S]), (c / S) & 1u, errors);
     if (KS > 1) {
       __syncwarp();
       cluster.sync();
@@ -224,17 +230,18 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
       float acc[BN];
 #pragma unroll
       for (int c = 0; c < BN; ++c) acc[c] = 0.0f;
-      float pre[kAhead][PL];  // xs * ws of the blocks ahead
-      auto load = [&](int b, float (&v)[PL]) {
-        const float w = b < b1 ? __ldg(wsp + b) : 0.0f;
+      // both scales of the blocks ahead, multiplied when used: a product here would wait for its loads
+      float px[kAhead][PL], pw[kAhead];
+      auto load = [&](int b, int a) {
+        pw[a] = b < b1 ? __ldg(wsp + b) : 0.0f;
 #pragma unroll
         for (int p = 0; p < PL; ++p) {
           const int c = lane + 32 * p;
-          v[p] = b < b1 && c < live ? w * __ldg(xs + b * rows + t.row + c) : 0.0f;
+          px[a][p] = b < b1 && c < live ? __ldg(xs + b * rows + t.row + c) : 0.0f;
         }
       };
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) load(b0 + a, pre[a]);
+      for (int a = 0; a < kAhead; ++a) load(b0 + a, a);
       for (int b = b0; b < b1 && ok; b += kAhead) {
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
@@ -242,11 +249,12 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
             float* line = scales[warp][a & 1];
 #pragma unroll
             for (int p = 0; p < PL; ++p)
-              if (lane + 32 * p < BN) line[lane + 32 * p] = pre[a][p];
-            load(b + a + kAhead, pre[a]);
+              if (lane + 32 * p < BN) line[lane + 32 * p] = px[a][p] * pw[a];
+            load(b + a + kAhead, a);
             const int pb = static_cast<int>(it % NB);
-            ok = bnn::tc::mbar_wait(smem_u32(&part_full[pb]), (it / NB) & 1u, &abort_flag, errors);
+            ok = bnn::fp8::wait(smem_u32(&part_full[pb]), (it / NB) & 1u, errors);
             ok = __all_sync(0xffffffffu, ok);
+            __syncwarp();  // every lane's part of `line` is written
             if (ok) {
               asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
 #pragma unroll
@@ -368,28 +376,57 @@ bnn_status narrow(const Args& a) {
   return launch_narrow<BN, 1, false>(a);
 }
 
+// The tile kernel's shape for `rows` rows in `groups` groups: least modelled
+// time, waves x (blocks of k x us a block + us a store), of the shapes that a
+// sweep over 64 .. 8192 rows x 4096 .. 11008 x 4096 (and 8192^3) left; the model
+// is within about 10% of what it chooses between.  Groups: 128-row tiles (a
+// pair's 256 rows end inside groups of a few hundred: 522 us against 416 at 64
+// groups, 16384 rows x 4096 x 4096) unless the groups are long.
+bnn_status gemm_tiles(const Args& a) {
+  struct Shape {
+    int ctas, tn;
+    double block_us, store_us;
+  };
+  static constexpr Shape kDense[] = {{1, 32, 0.156, 0.5}, {1, 64, 0.18, 1.0}, {1, 128, 0.26, 2.2}, {2, 256, 0.51, 3.0}};
+  static constexpr Shape kGrouped[] = {{1, 128, 0.26, 2.2}, {1, 256, 0.51, 3.0}, {2, 256, 0.51, 3.0}};
+  const bool grouped = a.offsets != nullptr;
+  const Shape* shapes = grouped ? kGrouped : kDense;
+  const int count = grouped ? 3 : 4;
+  const int64_t sms = bnn::sm_count(), busy = a.rows < a.groups ? a.rows : a.groups;
+  const Shape* best = shapes;
+  double best_us = 0.0;
+  for (int i = 0; i < count; ++i) {
+    const Shape& s = shapes[i];
+    const int64_t high = 128 * s.ctas, wide = (a.n + s.tn - 1) / s.tn, slots = sms / s.ctas;
+    // groups end inside a tile, in the mean half a tile each
+    const int64_t rtiles = grouped ? (a.rows + busy * high / 2) / high + 1 : (a.rows + high - 1) / high;
+    const int64_t waves = (rtiles * wide + slots - 1) / slots;
+    const double us = static_cast<double>(waves) * (a.kb * s.block_us + s.store_us);
+    if (i == 0 || us < best_us) {
+      best_us = us;
+      best = &s;
+    }
+  }
+  return bnn::fp8::gemm_tile(a, best->ctas, best->tn);
+}
+
+// Few rows (in the mean of the groups: their sizes are on the device): the
+// kernels that stream the weights.  Up to 8 rows and 2^26 bytes of weights the
+// register kernel (1 row, in us, against the tensor-memory one: 1024 x 1000 2.0
+// and 3.5, 4096 x 4096 5.6 and 6.5, 11008 x 4096 11.5 and 12.2, but 28672 x 8192
+// 54.7 and 41.4).  Above 32 rows the tile kernel (64 x 11008 x 4096: 14.3 us
+// against 16.7 with the weights on the lanes; but 32 x 4096 x 4096: 9.3 against
+// 7.7).
 bnn_status dispatch(const Args& a) {
   if (a.kb == 0) return gemm_empty(a);
-  const int64_t per = a.offsets ? (a.rows + a.groups - 1) / a.groups : a.rows;
-  if (per > 128) return bnn::fp8::gemm_pair(a);
-  return bnn::fp8::gemm_narrow(a);
+  const int64_t per = (a.rows + a.groups - 1) / a.groups;
+  if (!a.offsets && a.rows <= 8 && a.n * a.kb < (int64_t{1} << 19)) return bnn::fp8::gemm_skinny(a);
+  if (per <= 16) return narrow<16>(a);
+  if (per <= 32) return narrow<32>(a);
+  return gemm_tiles(a);
 }
 
 }  // namespace
-
-namespace bnn {
-namespace fp8 {
-
-bnn_status gemm_narrow(const Args& a) {
-  const int64_t per = a.offsets ? (a.rows + a.groups - 1) / a.groups : a.rows;
-  if (per <= 16) return narrow<16>(a);
-  if (per <= 32) return narrow<32>(a);
-  if (per <= 64) return narrow<64>(a);
-  return narrow<128>(a);
-}
-
-}  // namespace fp8
-}  // namespace bnn
 
 extern "C" bnn_status bnn_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                                    const float* bias, int64_t m, int64_t n, int64_t k, void* out, int out_type,

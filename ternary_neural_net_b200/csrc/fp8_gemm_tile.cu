@@ -1,0 +1,502 @@
+// The e4m3 matmul for more than a few rows: persistent CTAs, or CTA pairs, on
+// tiles of 128 or 256 rows x TN columns.
+//
+// Activation rows lie on the tensor-memory lanes (operand A, 128 rows per CTA),
+// TN weight rows are the MMA's N (a pair's halves in either CTA's shared
+// memory).  So in the epilogue a thread holds one activation row and TN / 2
+// columns of one weight scale block: the scale of a block of k is one number
+// per thread, and the block's sums cost one packed multiply-add per two
+// columns.  (With the weights on the lanes, as for few rows, every column has
+// a scale of its own: a shared-memory load per four columns, and shared memory
+// is what the operands already fill.)
+//
+// A ring stage holds U blocks of k (128 bytes a row each, one 3-D TMA box per
+// operand); each block's four MMAs of K = 32 start an accumulator of their own,
+// U x TN = 256 columns, two such sets in tensor memory.  While the epilogue
+// reads one set, scales it and adds it to its float32 registers, the tensor
+// cores fill the other.  What an iteration of a role costs is mostly the
+// latency of its hundred-odd dependent instructions (some 600 clocks measured
+// for the MMA warp and the copies alone), so narrow tiles take several blocks
+// per iteration.
+//
+// Roles per CTA: warps 0-7 epilogue (lane quarter w % 4, column half w / 4),
+// warp 8 TMA, warp 9 MMA (CTA 0's issues for a pair), warps 10 and 11 the
+// scales: they multiply the rows' with the weight blocks' into shared memory,
+// ahead.  A pair's copies complete on CTA 0's barriers.  Every wait is bounded;
+// a role whose wait runs out stops (and with it, by their own bounds, those
+// that wait for it), and the outputs are unspecified.
+#include <cooperative_groups.h>
+
+#include "fp8_common.cuh"
+
+namespace {
+
+using bnn::fp8::Args;
+using bnn::tc::mbar_expect_tx;
+using bnn::tc::smem_u32;
+using bnn::tc::sw128_desc;
+using bnn::tc::tmem_wait_ld;
+
+constexpr int kTm = 128;                       // activation rows per CTA
+constexpr int kBlockBytes = 128;               // bytes of a row's block of k
+constexpr int kScaleWarps = 2, kScaleAhead = 4;  // warps, and blocks whose scales are in flight
+constexpr int kScaleSlots = 4;                 // iterations whose scales are in shared memory
+constexpr int kBufs = 2;                       // accumulator sets
+constexpr int kEpiWarps = 8, kTmaWarp = kEpiWarps, kMmaWarp = kTmaWarp + 1, kScaleWarp = kTmaWarp + 2;
+constexpr int kThreads = 32 * (kEpiWarps + 4);
+constexpr int kStoreCols = 16;                 // columns per staged store step
+// Registers a thread: 168 at launch (three warps in each SM sub-partition's 16384), of
+// which the control warpgroup keeps 72 and each epilogue warpgroup takes 216.
+constexpr int kControlRegs = 72, kEpiRegs = 216;
+static_assert(128 * kControlRegs + 256 * kEpiRegs <= kThreads * 168, "register shares within the launch's");
+
+template <int CTAS, int TN>
+struct Cfg {
+  static constexpr int U = TN >= 64 ? 256 / TN : 4;                 // blocks of k per iteration
+  static constexpr int kWRows = TN / CTAS;                          // weight rows in a CTA's shared memory
+  static constexpr uint32_t kXBlock = kTm * kBlockBytes, kWBlock = kWRows * kBlockBytes;
+  static constexpr uint32_t kXBytes = U * kXBlock, kStageBytes = kXBytes + U * kWBlock;
+  static constexpr int kStages = 196608 / kStageBytes;              // 192 KiB of stages
+  static constexpr uint32_t kTmemCols = kBufs * U * TN;             // 512
+  static constexpr int kCols = TN / 2;                              // columns of an epilogue thread
+  static constexpr int kLoad = kCols < 32 || kCols > 64 ? 16 : 32;  // columns per load of tensor memory
+  static constexpr int kHalves = TN > 128 ? 2 : 1;                  // weight scale blocks of a tile
+  static constexpr size_t kSmem = kStages * kStageBytes + 1024;
+  static_assert(kWBlock % 1024 == 0, "swizzle atoms stay aligned");
+  static_assert(kScaleAhead % U == 0 && kStages >= 2, "");
+};
+
+// One box into this CTA's shared memory, its bytes completing on an mbarrier of
+// the cluster (a pair's CTA 0).
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* map, int y, int z, uint32_t bar0) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4}], [%5];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar0)
+      : "memory");
+}
+
+// Blocks [z, z + U) of rows [y, ..): out-of-range ones read as zero.
+template <int CTAS>
+__device__ __forceinline__ void load_box(uint32_t dst, const void* map, int y, int z, uint32_t bar) {
+  if constexpr (CTAS == 2)
+    tma_load_pair(dst, map, y, z, bar);
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void issue_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t word, uint32_t add) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"(add));
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"(add));
+}
+
+// Arrives on the mbarrier (in both CTAs of a pair) once the MMAs issued before have completed.
+template <int CTAS>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+            bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    bnn::tc::mma_commit(bar);
+}
+
+template <int N>
+__device__ __forceinline__ void load_cols(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 16)
+    bnn::tc::tmem_ld16(addr, r);
+  else
+    bnn::tc::tmem_ld32(addr, r);
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t s) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;\n" : "+l"(acc) : "l"(a), "l"(s));
+}
+
+template <int CTAS, int TN, bool GROUPED>
+__global__ void __launch_bounds__(kThreads, 1)
+fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                const float* __restrict__ xs, const float* __restrict__ ws, const float* __restrict__ bias,
+                const int64_t* __restrict__ offsets, int groups, int64_t rows, int64_t n, int kb,
+                void* __restrict__ out, int out_type, int wide, unsigned int* errors) {
+  namespace cg = cooperative_groups;
+  using C = Cfg<CTAS, TN>;
+  constexpr int S = C::kStages, U = C::U, CW = C::kCols, LD = C::kLoad, kRows = CTAS * kTm;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[S];   // a pair: CTA 0's, for both CTAs' copies
+  __shared__ __align__(8) uint64_t done_bar[S];   // the stage's MMAs: frees the stage, fills the accumulator
+  __shared__ __align__(8) uint64_t scale_bar[kScaleSlots];  // the iteration's scales are in `scales`
+  __shared__ __align__(8) uint64_t free_bar[kBufs];         // a pair: CTA 0's; one arrival per epilogue warp
+  __shared__ float scales[kScaleSlots][U][C::kHalves][kTm];
+  __shared__ float stage_out[kEpiWarps][32][kStoreCols + 1];
+  __shared__ uint32_t tmem_holder;
+  __shared__ bnn::fp8::Groups<GROUPED ? BNN_MAX_GROUPS : 1> map;
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = CTAS == 2 ? cg::this_cluster().block_rank() : 0;
+  const uint32_t ring = smem_u32(smem);
+  const int wtiles = static_cast<int>((n + TN - 1) / TN), its = (kb + U - 1) / U;
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      bnn::tc::mbar_init(smem_u32(&full_bar[i]), 1);
+      bnn::tc::mbar_init(smem_u32(&done_bar[i]), 1);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) bnn::tc::mbar_init(smem_u32(&scale_bar[i]), kScaleWarps);
+    for (int i = 0; i < kBufs; ++i) bnn::tc::mbar_init(smem_u32(&free_bar[i]), CTAS * kEpiWarps);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (tid == kTmaWarp * 32) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_x)) : "memory");
+  }
+  if (warp == kMmaWarp) {  // (the same warp of both CTAs of a pair)
+    if constexpr (CTAS == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&tmem_holder)),
+                   "r"(C::kTmemCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::);
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&tmem_holder)),
+                   "r"(C::kTmemCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
+    }
+  }
+  if (GROUPED) {
+    bnn::pdl_wait();  // the offsets may come from the preceding kernel
+    if (warp == 0) bnn::fp8::build_groups<kRows>(map, offsets, groups, rows, lane);
+  } else if (tid == 0) {
+    map.start[0] = 0;
+    map.start[1] = static_cast<int>(rows);
+    map.first[0] = 0;
+    map.first[1] = static_cast<int>((rows + kRows - 1) / kRows);
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+  __syncthreads();
+  if constexpr (CTAS == 2) cg::this_cluster().sync();  // both CTAs' barriers exist before any copy or arrival
+  asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+  const uint32_t tmem = tmem_holder;
+  bnn::pdl_trigger();
+  const int64_t tiles = static_cast<int64_t>(map.first[groups]) * wtiles;
+  const int64_t step = gridDim.x / CTAS, tile0 = blockIdx.x / CTAS;
+
+  if (warp >= kEpiWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kControlRegs));
+    const uint32_t full = smem_u32(full_bar), done = smem_u32(done_bar);
+    if (warp == kTmaWarp) {
+      // ---------------------------------------------------------- TMA copies
+      uint32_t full0 = full;  // a pair's: CTA 0's
+      if constexpr (CTAS == 2) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(full0) : "r"(full));
+      bnn::fp8::Ring<S> st;
+      bool ok = true, waited = GROUPED;
+      for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+        const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map.start, map.first, wtiles);
+        const int xrow = t.row + kTm * static_cast<int>(rank);
+        const int wrow = t.group * static_cast<int>(n) + t.wtile * TN + C::kWRows * static_cast<int>(rank);
+        int ahead = 0;  // stages whose weights are already on their way
+        if (!waited) {
+          ahead = min(S, its);
+          if (bnn::fp8::elected()) {
+            for (int i = 0; i < ahead; ++i) {
+              if (rank == 0) mbar_expect_tx(full + 8 * i, CTAS * C::kStageBytes);
+              load_box<CTAS>(ring + i * C::kStageBytes + C::kXBytes, &tmap_w, wrow, i * U, full0 + 8 * i);
+            }
+          }
+          __syncwarp();
+          bnn::pdl_wait();
+          waited = true;
+        }
+        for (int b = 0; b < its; ++b, st.next()) {
+          // (the round before a barrier's first counts as done)
+          ok = bnn::fp8::wait(done + 8 * st.at, st.round ^ 1u, errors);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          if (bnn::fp8::elected()) {
+            const uint32_t dst = ring + st.at * C::kStageBytes, bar = full0 + 8 * st.at;
+            if (b >= ahead) {
+              if (rank == 0) mbar_expect_tx(full + 8 * st.at, CTAS * C::kStageBytes);
+              load_box<CTAS>(dst + C::kXBytes, &tmap_w, wrow, b * U, bar);
+            }
+            load_box<CTAS>(dst, &tmap_x, xrow, b * U, bar);
+          }
+          __syncwarp();
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (!waited) bnn::pdl_wait();
+      // The CTA must not retire with copies in flight: every stage's last MMAs are waited for (they follow its
+      // copies).
+      for (int i = 0; i < S; ++i, st.next()) bnn::fp8::wait(done + 8 * st.at, st.round ^ 1u, errors);
+    } else if (warp == kMmaWarp && rank == 0) {
+      // ---------------------------------------------------------- MMA issue
+      if (!GROUPED) bnn::pdl_wait();  // before the first bounded wait (for copies that start after it)
+      constexpr uint32_t word = bnn::fp8::mma_word(kRows, TN);
+      const uint32_t freed = smem_u32(free_bar);
+      const uint64_t desc = sw128_desc(ring);
+      bnn::fp8::Ring<S> st;
+      bnn::fp8::Ring<kBufs> acc;
+      bool ok = true;
+      for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+        for (int b = 0; b < its; ++b, st.next(), acc.next()) {
+          ok = bnn::fp8::wait2(freed + 8 * acc.at, acc.round ^ 1u, full + 8 * st.at, st.round, errors);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+          if (bnn::fp8::elected()) {
+            const uint64_t ad = desc + st.at * (C::kStageBytes >> 4), bd = ad + (C::kXBytes >> 4);
+            const uint32_t d = tmem + acc.at * (U * TN);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                issue_mma<CTAS>(d + u * TN, ad + (u * (C::kXBlock >> 4) + 2 * kk), bd + (u * (C::kWBlock >> 4) + 2 * kk),
+                                word, kk > 0 ? 1u : 0u);
+            commit<CTAS>(done + 8 * st.at);
+          }
+          __syncwarp();
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    } else if (warp >= kScaleWarp) {
+      // ---------------------------------------------------------- scales
+      // Per block of k: xs of 64 of this CTA's rows (two a lane) times ws of the tile's weight blocks.
+      if (!GROUPED) bnn::pdl_wait();
+      const uint32_t ready = smem_u32(scale_bar);
+      const int r0 = 64 * (warp - kScaleWarp) + lane, nb = static_cast<int>((n + 127) / 128);
+      // Before iteration i's scales are written, iteration i - kScaleSlots's must have been read.  A CTA on its own
+      // waits until iteration i - kBufs has been read: the next phase of that barrier is iteration i's, which needs
+      // these scales, so it cannot be missed.  In a pair, whose barrier for that is CTA 0's, it waits for the MMAs of
+      // i - kBufs, which follow the reading of i - 2 kBufs; their barrier's next phase is S iterations on.
+      static_assert(CTAS == 1 || S >= 2 * kBufs, "the next phase needs iteration i's scales");
+      static_assert(kScaleSlots == 2 * kBufs, "");
+      bnn::fp8::Ring<kScaleSlots> st;
+      bnn::fp8::Ring<CTAS == 1 ? kBufs : S> old;
+      const uint32_t read = CTAS == 1 ? smem_u32(free_bar) : done;
+      bool ok = true;
+      int lead = kBufs;
+      for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+        const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map.start, map.first, wtiles);
+        const int row = t.row + kTm * static_cast<int>(rank) + r0;
+        const int live = t.end - row, wb = t.wtile * TN / 128;
+        const bool two = C::kHalves == 2 && wb + 1 < nb;
+        const float* wsp = ws + (static_cast<int64_t>(t.group) * nb + wb) * kb;
+        const float* xsp = xs + row;
+        float x[kScaleAhead][2], w[kScaleAhead][2];
+        int next = 0;  // block the pointers stand at
+        auto load = [&](int a) {
+          const bool more = next < kb;
+          x[a][0] = more && live > 0 ? __ldg(xsp) : 0.0f;
+          x[a][1] = more && live > 32 ? __ldg(xsp + 32) : 0.0f;
+          w[a][0] = more ? __ldg(wsp) : 0.0f;
+          if (C::kHalves == 2) w[a][1] = more && two ? __ldg(wsp + kb) : 0.0f;
+          xsp += rows;
+          ++wsp;
+          ++next;
+        };
+#pragma unroll
+        for (int a = 0; a < kScaleAhead; ++a) load(a);
+        for (int b = 0; b < its && ok; b += kScaleAhead / U) {
+#pragma unroll
+          for (int a = 0; a < kScaleAhead; a += U) {
+            if (b + a / U < its && ok) {
+              if (lead > 0) {
+                --lead;
+              } else {
+                ok = bnn::fp8::wait(read + 8 * old.at, old.round, errors);
+                old.next();
+              }
+              ok = __all_sync(0xffffffffu, ok);
+              if (ok) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                      scales[st.at][u][h][r0 + 32 * i] = x[a + u][i] * w[a + u][h];
+                  load(a + u);
+                }
+                __syncwarp();
+                if (bnn::fp8::elected()) bnn::tc::mbar_arrive(ready + 8 * st.at);
+                __syncwarp();
+                st.next();
+              }
+            }
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kEpiRegs));
+    // ------------------------------------------------------------ scale and add
+    if (!GROUPED) bnn::pdl_wait();
+    const int q = warp & 3, part = warp >> 2;
+    const uint32_t src0 = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(part * CW);
+    const uint32_t done = smem_u32(done_bar), ready = smem_u32(scale_bar);
+    uint32_t freed0 = smem_u32(free_bar);  // a pair's: CTA 0's
+    if constexpr (CTAS == 2) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(freed0) : "r"(smem_u32(free_bar)));
+    auto release = [&](uint32_t buf) {  // this warp has the accumulator in registers
+      asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+      __syncwarp();
+      if (bnn::fp8::elected()) {
+        if constexpr (CTAS == 2)
+          bnn::fp8::arrive_cluster(freed0 + 8 * buf);
+        else
+          bnn::tc::mbar_arrive(freed0 + 8 * buf);
+      }
+      __syncwarp();
+    };
+    bnn::fp8::Ring<S> st;
+    bnn::fp8::Ring<kScaleSlots> sl;
+    uint32_t buf = 0;
+    bool ok = true;
+    for (int64_t tile = tile0; tile < tiles; tile += step) {
+      uint64_t acc[CW / 2];
+#pragma unroll
+      for (int c = 0; c < CW / 2; ++c) acc[c] = 0;
+      for (int b = 0; b < its; ++b, st.next(), sl.next(), buf ^= 1u) {
+        ok = bnn::fp8::wait2(done + 8 * st.at, st.round, ready + 8 * sl.at, sl.round, errors);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+        const uint32_t src = src0 + buf * (U * TN);
+        const float* sc = &scales[sl.at][0][C::kHalves == 2 ? part : 0][32 * q + lane];
+        uint32_t r[2][LD];
+        load_cols<LD>(src, r[0]);
+        uint64_t s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) s[u] = pack2(sc[u * C::kHalves * kTm], sc[u * C::kHalves * kTm]);
+#pragma unroll
+        for (int c0 = 0; c0 < U * CW; c0 += LD) {  // LD columns at a time, the next ones on their way
+          const int i = (c0 / LD) & 1, next = c0 + LD, c = c0 % CW;
+          tmem_wait_ld();
+          if (next < U * CW)
+            load_cols<LD>(src + next / CW * TN + next % CW, r[i ^ 1]);
+          else
+            release(buf);
+#pragma unroll
+          for (int j = 0; j < LD; j += 2)
+            fma2(acc[(c + j) / 2], pack2(__uint_as_float(r[i][j]), __uint_as_float(r[i][j + 1])),
+                 s[c0 / CW]);
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      // ---------------------------------------------------------- store
+      const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map.start, map.first, wtiles);
+      const int64_t row0 = t.row + kTm * static_cast<int>(rank) + 32 * q;  // this warp's first row
+      const int64_t j0 = static_cast<int64_t>(t.wtile) * TN + part * CW;
+      const int live = static_cast<int>(min(int64_t{32}, t.end - row0));
+      if (live <= 0 || j0 >= n) continue;
+      if (wide && j0 + CW <= n) {
+        const int64_t at = (row0 + lane) * n + j0;
+#pragma unroll
+        for (int c = 0; c < CW; c += 8) {
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) unpack2(acc[(c + i) / 2], y[i], y[i + 1]);
+          if (bias) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] += __ldg(bias + j0 + c + i);
+          }
+          if (lane < live) bnn::fp8::store_eight(out, out_type, at + c, y);
+        }
+      } else {
+        // Rows whose starts 16-byte stores cannot take, or a tile that ends inside: a few columns at a time through
+        // shared memory, so that a warp stores a few rows' pieces side by side instead of 32 rows' single elements.
+#pragma unroll
+        for (int c = 0; c < CW; c += kStoreCols) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kStoreCols; i += 2) {
+            float y0, y1;
+            unpack2(acc[(c + i) / 2], y0, y1);
+            stage_out[warp][lane][i] = y0;
+            stage_out[warp][lane][i + 1] = y1;
+          }
+          __syncwarp();
+          const int64_t j = j0 + c + lane % kStoreCols;
+          const float bj = bias && j < n ? __ldg(bias + j) : 0.0f;
+          if (j < n)
+            for (int r = lane / kStoreCols; r < live; r += 32 / kStoreCols)
+              bnn::fp8::store_one(out, out_type, (row0 + r) * n + j, stage_out[warp][r][lane % kStoreCols] + bj);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+  __syncthreads();
+  if constexpr (CTAS == 2) {
+    cg::this_cluster().sync();  // neither CTA leaves while the pair's tensor memory or barriers are in use
+    if (warp == kMmaWarp)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::kTmemCols));
+  } else {
+    if (warp == kMmaWarp)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::kTmemCols));
+  }
+}
+
+template <int CTAS, int TN, bool GROUPED>
+bnn_status launch(const Args& a) {
+  using C = Cfg<CTAS, TN>;
+  constexpr int kRows = CTAS * kTm;
+  const int64_t wtiles = (a.n + TN - 1) / TN;
+  // groups: at most one ragged tile each beside the full ones
+  const int64_t rtiles =
+      GROUPED ? a.rows / kRows + (a.rows < a.groups ? a.rows : a.groups) : (a.rows + kRows - 1) / kRows;
+  const int64_t tiles = rtiles * wtiles, slots = bnn::sm_count() / CTAS;
+  const int64_t units = tiles < slots ? tiles : slots;
+  CUtensorMap tw, tx;
+  const uint64_t kb = static_cast<uint64_t>(a.kb);
+  if (!bnn::encode_tmap_blocks(&tw, a.wq, static_cast<uint64_t>(a.groups * a.n), kb, C::kWRows, C::U) ||
+      !bnn::encode_tmap_blocks(&tx, a.xq, static_cast<uint64_t>(a.rows), kb, kTm, C::U))
+    return BNN_ERR_UNSUPPORTED;
+  unsigned int* errors = bnn::device_error_counter();
+  if (!errors) return bnn::cuda_fail(cudaGetLastError());
+  // 16-byte stores need every row's start aligned
+  const int wide = bnn::aligned(a.out, 16) && a.n * static_cast<int64_t>(bnn::fp8::type_size(a.out_type)) % 16 == 0;
+  auto kern = fp8_tile_kernel<CTAS, TN, GROUPED>;
+  BNN_TRY(bnn::ensure_smem(kern, C::kSmem));
+  const cudaError_t e = bnn::launch_pdl(kern, dim3(static_cast<unsigned>(CTAS * units)), dim3(kThreads), C::kSmem,
+                                        a.stream, CTAS, tw, tx, a.xs, a.ws, a.bias, a.offsets, a.groups, a.rows, a.n,
+                                        a.kb, a.out, a.out_type, wide, errors);
+  if (e != cudaSuccess) return bnn::cuda_fail(e);
+  return bnn::check_launch();
+}
+
+}  // namespace
+
+namespace bnn {
+namespace fp8 {
+
+bnn_status gemm_tile(const Args& a, int ctas, int tn) {
+  if (a.offsets) {
+    if (ctas == 2) return launch<2, 256, true>(a);
+    return tn == 256 ? launch<1, 256, true>(a) : launch<1, 128, true>(a);
+  }
+  if (ctas == 2) return launch<2, 256, false>(a);
+  return tn == 256 ? launch<1, 256, false>(a) : tn == 128 ? launch<1, 128, false>(a) : tn == 32 ? launch<1, 32, false>(a) : launch<1, 64, false>(a);
+}
+
+}  // namespace fp8
+}  // namespace bnn
