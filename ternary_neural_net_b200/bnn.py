@@ -383,6 +383,12 @@ def fp8_blocks(k: int) -> int:
     return (k + 127) // 128
 
 
+# The current stream's handle by device index: the raw getter where this PyTorch has it (it saves a Stream
+# object, more than a microsecond, per call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _fp8_call(name, call, device, *args):
     """call(*args, stream) with the operands' device current; tensors go as their pointers, None as NULL.
     (A decoding step makes hundreds of these calls, each of a few microseconds on the GPU.)"""
@@ -391,7 +397,7 @@ def _fp8_call(name, call, device, *args):
     if before != index:
         torch.cuda.set_device(index)
     try:
-        st = call(*args, torch.cuda.current_stream(index).cuda_stream)
+        st = call(*args, _raw_stream(index))
     finally:
         if before != index:
             torch.cuda.set_device(before)

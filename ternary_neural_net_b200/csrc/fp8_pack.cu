@@ -34,59 +34,90 @@ struct Lane {
   static constexpr int kBlocks = 32 / kLanes;   // blocks of one row that a warp takes at once
 };
 
-__device__ __forceinline__ void to_f32(const float (&v)[4], float (&f)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = v[i];
-}
-__device__ __forceinline__ void to_f32(const __nv_bfloat16 (&v)[8], float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __bfloat162float(v[i]);
-}
-__device__ __forceinline__ void to_f32(const __half (&v)[8], float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __half2float(v[i]);
-}
+// A lane's 16 bytes of input as four words.
+struct Words {
+  uint32_t w[4];
+};
 
-// V-element vector loads of the lane's E elements starting at element e of a
-// row of k elements (k % V == 0 and the row V-aligned); 0 past k.
-template <typename T, int V>
-__device__ __forceinline__ void load_lane(const T* row, int64_t e, int64_t k, T (&v)[Lane<T>::E]) {
-  struct alignas(V * sizeof(T)) Vec {
-    T x[V];
-  };
+// Word i as one float32 or two 16-bit elements.
+__device__ __forceinline__ void to_f32(const Words& v, float (&f)[4], float) {
 #pragma unroll
-  for (int i = 0; i < Lane<T>::E; i += V) {
-    Vec t;
-    if (e + i < k) {
-      t = *reinterpret_cast<const Vec*>(row + e + i);
-    } else {
+  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v.w[i]);
+}
+__device__ __forceinline__ void to_f32(const Words& v, float (&f)[8], __nv_bfloat16) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) t.x[j] = static_cast<T>(0.0f);
-    }
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(v.w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v.w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void to_f32(const Words& v, float (&f)[8], __half) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[i + j] = t.x[j];
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __half2float(__ushort_as_half(static_cast<unsigned short>(v.w[i] & 0xffffu)));
+    f[2 * i + 1] = __half2float(__ushort_as_half(static_cast<unsigned short>(v.w[i] >> 16)));
   }
 }
 
-template <int E>
-__device__ __forceinline__ uint32_t top_bits(const float (&f)[E]) {
-  uint32_t a = 0;
+// The lane's elements from element e of a row of k on, in loads of V elements
+// (k % V == 0 and the row V-aligned); 0 past k.
+template <typename T, int V>
+__device__ __forceinline__ Words load_lane(const T* row, int64_t e, int64_t k) {
+  Words v;
+  const T* p = row + e;
+  if constexpr (V * sizeof(T) == 16) {
+    const uint4 x = e < k ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+    v.w[0] = x.x, v.w[1] = x.y, v.w[2] = x.z, v.w[3] = x.w;
+  } else if constexpr (V * sizeof(T) == 8) {
 #pragma unroll
-  for (int i = 0; i < E; ++i) a = max(a, __float_as_uint(f[i]) & 0x7fffffffu);
+    for (int i = 0; i < 2; ++i) {
+      const uint2 x = e + i * V < k ? *reinterpret_cast<const uint2*>(p + i * V) : make_uint2(0, 0);
+      v.w[2 * i] = x.x, v.w[2 * i + 1] = x.y;
+    }
+  } else if constexpr (V * sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.w[i] = e + i * V < k ? *reinterpret_cast<const uint32_t*>(p + i * V) : 0u;
+  } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = e + 2 * i < k ? h[2 * i] : 0u, hi = e + 2 * i + 1 < k ? h[2 * i + 1] : 0u;
+      v.w[i] = lo | (hi << 16);
+    }
+  }
+  return v;
+}
+
+// Largest absolute value among a lane's elements so far, `a`, and those of `v`,
+// as bit patterns without the sign: float32, or two 16-bit elements compared at
+// a time.  bits_of then gives the float32 bits.
+__device__ __forceinline__ uint32_t top(uint32_t a, const Words& v, float) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a = max(a, v.w[i] & 0x7fffffffu);
   return a;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t top(uint32_t a, const Words& v, T) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a = __vmaxu2(a, v.w[i] & 0x7fff7fffu);
+  return a;
+}
+__device__ __forceinline__ uint32_t bits_of(uint32_t a, float) { return a; }
+__device__ __forceinline__ uint32_t bits_of(uint32_t a, __nv_bfloat16) { return max(a & 0xffffu, a >> 16) << 16; }
+__device__ __forceinline__ uint32_t bits_of(uint32_t a, __half) {
+  return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(max(a & 0xffffu, a >> 16)))));
 }
 
 struct Scale {
-  float scale, factor;
-  bool fine;
+  float scale, factor;  // factor 0: the block holds an infinity or a NaN
 };
 
 __device__ __forceinline__ Scale scale_of(uint32_t bits) {
   Scale s;
-  s.fine = bits < kInfBits;
-  const float a = s.fine ? fmaxf(__uint_as_float(bits), 0x1p-100f) : 1.0f;
-  s.scale = s.fine ? __fdiv_rn(a, kTop) : __int_as_float(0x7fffffff);
-  s.factor = __fdiv_rn(kTop, a);
+  const bool fine = bits < kInfBits;
+  const float a = fine ? fmaxf(__uint_as_float(bits), 0x1p-100f) : 1.0f;
+  s.scale = fine ? __fdiv_rn(a, kTop) : __int_as_float(0x7fffffff);
+  s.factor = fine ? __fdiv_rn(kTop, a) : 0.0f;
   return s;
 }
 
@@ -98,104 +129,104 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, f
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-__device__ __forceinline__ void store_lane(uint8_t* dst, const float (&f)[4], const Scale& s) {
-  *reinterpret_cast<uint32_t*>(dst) = s.fine ? e4m3x4(f[0], f[1], f[2], f[3], s.factor) : 0u;
+__device__ __forceinline__ void store_lane(uint8_t* dst, const float (&f)[4], float r) {
+  *reinterpret_cast<uint32_t*>(dst) = r != 0.0f ? e4m3x4(f[0], f[1], f[2], f[3], r) : 0u;
 }
-__device__ __forceinline__ void store_lane(uint8_t* dst, const float (&f)[8], const Scale& s) {
+__device__ __forceinline__ void store_lane(uint8_t* dst, const float (&f)[8], float r) {
   uint2 v = make_uint2(0u, 0u);
-  if (s.fine) v = make_uint2(e4m3x4(f[0], f[1], f[2], f[3], s.factor), e4m3x4(f[4], f[5], f[6], f[7], s.factor));
+  if (r != 0.0f) v = make_uint2(e4m3x4(f[0], f[1], f[2], f[3], r), e4m3x4(f[4], f[5], f[6], f[7], r));
   *reinterpret_cast<uint2*>(dst) = v;
 }
 
-// Rows.  A CTA takes 32 rows x kBlocks blocks, a warp four of the rows: the four
-// rows' 16-byte loads are in flight together, and the CTA's scales (32 rows of a
-// block) leave as one 128-byte line of the block-major scale matrix.
-constexpr int kRowsPerWarp = 4;
-constexpr int kTileRows = kWarps * kRowsPerWarp;
+// Rows.  A warp takes one row x kSteps consecutive steps of kBlocks blocks: its
+// 16-byte loads are in flight together and read the row contiguously.  A CTA's
+// eight rows' scales leave as 32-byte pieces of the block-major scale matrix.
+constexpr int kSteps = 4;
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads)
 fp8_pack_rows_kernel(const T* __restrict__ x, int64_t x_rows, const int32_t* __restrict__ index, int64_t rows,
                      int64_t k, int64_t kb, int64_t col_tiles, uint8_t* __restrict__ q, float* __restrict__ scale) {
   using L = Lane<T>;
-  __shared__ float sc[L::kBlocks][kTileRows];
+  constexpr int kTileBlocks = kSteps * L::kBlocks;
+  __shared__ float sc[kTileBlocks][kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tile_row = (blockIdx.x / col_tiles) * kTileRows;
-  const int64_t b = (blockIdx.x % col_tiles) * L::kBlocks + lane / L::kLanes;  // this lane's block
-  const int64_t e = b * 128 + (lane % L::kLanes) * L::E;
+  const int64_t tile_row = (blockIdx.x / col_tiles) * kWarps, row = tile_row + warp;
+  const int64_t b0 = (blockIdx.x % col_tiles) * kTileBlocks;
+  const int64_t e0 = b0 * 128 + lane * L::E;
   bnn::pdl_trigger();  // a matmul launched after this kernel may start on its weights now
-  T v[kRowsPerWarp][L::E];
+  int64_t src = row;
+  if (index) src = row < rows ? static_cast<int64_t>(__ldg(index + row)) : -1;
+  const bool live = row < rows && src >= 0 && src < x_rows;
+  Words v[kSteps];
 #pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i) {
-    const int64_t row = tile_row + warp * kRowsPerWarp + i;
-    int64_t src = row;
-    if (index) src = row < rows ? static_cast<int64_t>(__ldg(index + row)) : -1;
-    const bool live = row < rows && src >= 0 && src < x_rows;
-    load_lane<T, V>(x + (live ? src : 0) * k, live ? e : k, k, v[i]);
-  }
+  for (int i = 0; i < kSteps; ++i) v[i] = load_lane<T, V>(x + (live ? src : 0) * k, live ? e0 + i * 32 * L::E : k, k);
+  // The steps' maxima, then both divisions once for all of the warp's blocks: lane i of each block's lanes takes
+  // step i.
+  uint32_t mine = 0;
 #pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i) {
-    const int r = warp * kRowsPerWarp + i;
-    float f[L::E];
-    to_f32(v[i], f);
-    uint32_t a = top_bits(f);
+  for (int i = 0; i < kSteps; ++i) {
+    uint32_t a = bits_of(top(0u, v[i], T{}), T{});
 #pragma unroll
     for (int off = L::kLanes / 2; off > 0; off >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
-    const Scale s = scale_of(a);
-    if (tile_row + r < rows && b < kb) store_lane(q + (tile_row + r) * kb * 128 + e, f, s);
-    if (lane % L::kLanes == 0) sc[lane / L::kLanes][r] = s.scale;
+    if (lane % L::kLanes == i) mine = a;
+  }
+  const Scale s = scale_of(mine);
+  if (lane % L::kLanes < kSteps) sc[lane % L::kLanes * L::kBlocks + lane / L::kLanes][warp] = s.scale;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const float r = __shfl_sync(0xffffffffu, s.factor, i, L::kLanes);
+    float f[L::E];
+    to_f32(v[i], f, T{});
+    if (row < rows && b0 + i * L::kBlocks + lane / L::kLanes < kb)
+      store_lane(q + row * kb * 128 + e0 + i * 32 * L::E, f, r);
   }
   __syncthreads();
-  if (warp < L::kBlocks) {
-    const int64_t sb = (blockIdx.x % col_tiles) * L::kBlocks + warp;
-    if (sb < kb && tile_row + lane < rows) scale[sb * rows + tile_row + lane] = sc[warp][lane];
-  }
+  const int b = threadIdx.x / kWarps, r = threadIdx.x % kWarps;
+  if (b < kTileBlocks && b0 + b < kb && tile_row + r < rows) scale[(b0 + b) * rows + tile_row + r] = sc[b][r];
 }
 
-// Weights.  A CTA takes one 128 x 128 block whole in registers (16 bytes a lane
-// and load, 8 or 16 loads), a warp 16 of its rows.
+// Weights.  A CTA takes 128 rows x kBlocks blocks (512 bytes of a row) whole in
+// registers, a warp 16 of the rows, one 16-byte load a lane for each.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads)
-fp8_pack_weight_kernel(const T* __restrict__ w, int64_t n, int64_t k, int64_t kb, int64_t nb, uint8_t* __restrict__ q,
-                       float* __restrict__ scale) {
+__global__ void __launch_bounds__(kThreads, V * sizeof(T) >= 8 ? 3 : 2)
+fp8_pack_weight_kernel(const T* __restrict__ w, int64_t n, int64_t k, int64_t kb, int64_t nb, int64_t col_tiles,
+                       uint8_t* __restrict__ q, float* __restrict__ scale) {
   using L = Lane<T>;
-  constexpr int kRows = 128 / kWarps;          // rows of a warp
-  constexpr int kLoads = kRows / L::kBlocks;   // a load covers kBlocks rows
-  __shared__ uint32_t tops[kWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t b = blockIdx.x % kb, t = blockIdx.x / kb, j0 = (t % nb) * 128, g = t / nb;
-  const int64_t e = b * 128 + (lane % L::kLanes) * L::E;
-  const int64_t row0 = j0 + warp * kRows + lane / L::kLanes;
+  constexpr int kRows = 128 / kWarps;  // rows of a warp
+  __shared__ uint32_t tops[kWarps][L::kBlocks];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, blk = lane / L::kLanes;
+  const int64_t t = blockIdx.x / col_tiles, j0 = (t % nb) * 128, g = t / nb;
+  const int64_t b0 = (blockIdx.x % col_tiles) * L::kBlocks, e = b0 * 128 + lane * L::E;
+  const int64_t row0 = j0 + warp * kRows;
   const T* base = w + g * n * k;
-  T v[kLoads][L::E];
+  Words v[kRows];
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int64_t row = row0 + i * L::kBlocks;
-    const bool live = row < n;
-    load_lane<T, V>(base + (live ? row : 0) * k, live ? e : k, k, v[i]);
+  for (int i = 0; i < kRows; ++i) {
+    const bool live = row0 + i < n;
+    v[i] = load_lane<T, V>(base + (live ? row0 + i : 0) * k, live ? e : k, k);
   }
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    float f[L::E];
-    to_f32(v[i], f);
-    a = max(a, top_bits(f));
-  }
-  a = __reduce_max_sync(0xffffffffu, a);
-  if (lane == 0) tops[warp] = a;
+  for (int i = 0; i < kRows; ++i) a = top(a, v[i], T{});
+  a = bits_of(a, T{});
+#pragma unroll
+  for (int off = L::kLanes / 2; off > 0; off >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
+  if (lane % L::kLanes == 0) tops[warp][blk] = a;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) a = max(a, tops[i]);
+  for (int i = 0; i < kWarps; ++i) a = max(a, tops[i][blk]);
   const Scale s = scale_of(a);
   uint8_t* dst = q + g * n * kb * 128;
+  if (b0 + blk < kb) {
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int64_t row = row0 + i * L::kBlocks;
-    float f[L::E];
-    to_f32(v[i], f);
-    if (row < n) store_lane(dst + row * kb * 128 + e, f, s);
+    for (int i = 0; i < kRows; ++i) {
+      float f[L::E];
+      to_f32(v[i], f, T{});
+      if (row0 + i < n) store_lane(dst + (row0 + i) * kb * 128 + e, f, s.factor);
+    }
+    if (warp == 0 && lane % L::kLanes == 0) scale[(g * nb + j0 / 128) * kb + b0 + blk] = s.scale;
   }
-  if (threadIdx.x == 0) scale[(g * nb + j0 / 128) * kb + b] = s.scale;
 }
 
 // Launched after the weight pack: see bnn_fp8_pack_weight.
@@ -212,8 +243,9 @@ int vec_of(const void* p, int64_t k) {
 template <typename T, int V>
 bnn_status launch_rows(const T* x, int64_t x_rows, const int32_t* index, int64_t rows, int64_t k, uint8_t* q,
                        float* scale, cudaStream_t s) {
-  const int64_t kb = (k + 127) / 128, col_tiles = (kb + Lane<T>::kBlocks - 1) / Lane<T>::kBlocks;
-  const int64_t grid = (rows + kTileRows - 1) / kTileRows * col_tiles;
+  constexpr int kTileBlocks = kSteps * Lane<T>::kBlocks;
+  const int64_t kb = (k + 127) / 128, col_tiles = (kb + kTileBlocks - 1) / kTileBlocks;
+  const int64_t grid = (rows + kWarps - 1) / kWarps * col_tiles;
   if (grid > INT32_MAX) return BNN_ERR_INVALID_ARG;
   fp8_pack_rows_kernel<T, V><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(x, x_rows, index, rows, k, kb, col_tiles,
                                                                              q, scale);
@@ -235,9 +267,10 @@ bnn_status pack_rows(const void* xv, int64_t x_rows, const int32_t* index, int64
 
 template <typename T, int V>
 bnn_status launch_weight(const T* w, int64_t groups, int64_t n, int64_t k, uint8_t* q, float* scale, cudaStream_t s) {
-  const int64_t kb = (k + 127) / 128, nb = (n + 127) / 128, grid = groups * nb * kb;
+  const int64_t kb = (k + 127) / 128, nb = (n + 127) / 128, col_tiles = (kb + Lane<T>::kBlocks - 1) / Lane<T>::kBlocks;
+  const int64_t grid = groups * nb * col_tiles;
   if (grid > INT32_MAX) return BNN_ERR_INVALID_ARG;
-  fp8_pack_weight_kernel<T, V><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(w, n, k, kb, nb, q, scale);
+  fp8_pack_weight_kernel<T, V><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(w, n, k, kb, nb, col_tiles, q, scale);
   fp8_settle_kernel<<<1, 1, 0, s>>>();
   return bnn::check_launch();
 }
