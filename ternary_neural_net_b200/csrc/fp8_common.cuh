@@ -32,45 +32,35 @@ bnn_status gemm_skinny(const Args& a);
 // Tiles of 128 (ctas = 1) or 256 rows (a CTA pair) x tn columns.
 bnn_status gemm_tile(const Args& a, int ctas, int tn);
 
-// Bounded wait for an mbarrier phase: up to kPolls polls in a loop of four
-// instructions.  (bnn::tc::mbar_wait bounds by the wall clock; its code around
-// every wait costs these kernels, which wait twice per block of k and role, more
-// than the waits themselves; and polls with a time hint wake hundreds of clocks
-// late.)  Every thread has waited for the kernel ahead before its first call, so
-// only copies and MMAs of this kernel are waited for: microseconds, against
-// 10 ms of polls at the least.  False when it ran out: counted in *errors by
-// each thread.
+// Bounded wait of a whole converged warp for an mbarrier phase: up to kPolls
+// polls, each a try_wait and a vote, so that the branch is uniform.  (A wait on
+// a completed phase takes some 70 clocks like this and about 130 as a loop that
+// each lane leaves by itself; bnn::tc::mbar_wait, which bounds by the wall
+// clock, takes longer still, and polls with a time hint wake hundreds of clocks
+// late.  These kernels wait twice per block of k and role.)  Every thread has
+// waited for the kernel ahead before its first call, so only copies and MMAs of
+// this kernel are waited for: microseconds, against 30 ms of polls at the least.
+// False, for the whole warp, when it ran out: counted in *errors by each thread.
 constexpr uint32_t kPolls = 1u << 20;
 
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, unsigned int* errors) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p, q;\n.reg .u32 i;\nmov.u32 i, 0;\n"
-      "POLL:\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n@p bra DONE;\n"
-      "add.u32 i, i, 1;\nsetp.lt.u32 q, i, %3;\n@q bra POLL;\n"
-      "DONE:\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "n"(kPolls)
-      : "memory");
-  if (!ok) atomicAdd(errors, 1u);
-  return ok != 0;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kPolls; ++i)
+    if (__all_sync(0xffffffffu, tc::mbar_try(bar, parity))) return true;
+  atomicAdd(errors, 1u);
+  return false;
 }
 
 // The same for two barriers at once: the polls' latencies overlap.
 __device__ __forceinline__ bool wait2(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b,
                                       unsigned int* errors) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p, q;\n.reg .u32 i;\nmov.u32 i, 0;\n"
-      "POLL:\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\nand.pred p, p, q;\n@p bra DONE;\n"
-      "add.u32 i, i, 1;\nsetp.lt.u32 q, i, %5;\n@q bra POLL;\n"
-      "DONE:\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar_a), "r"(parity_a), "r"(bar_b), "r"(parity_b), "n"(kPolls)
-      : "memory");
-  if (!ok) atomicAdd(errors, 1u);
-  return ok != 0;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kPolls; ++i) {
+    const bool a = tc::mbar_try(bar_a, parity_a), b = tc::mbar_try(bar_b, parity_b);
+    if (__all_sync(0xffffffffu, a && b)) return true;
+  }
+  atomicAdd(errors, 1u);
+  return false;
 }
 
 // Position in a ring of N slots and the parity of its current round.
@@ -85,41 +75,112 @@ struct Ring {
   }
 };
 
-// True in one thread of a converged warp (the same one each time).  The copy and
-// MMA warps run their loops as whole warps and issue inside if (elected()): a
-// loop that one lane runs by itself takes several times as long per wait and
-// per issue, since these instructions take warp-uniform operands.
-__device__ __forceinline__ bool elected() {
+// 1 in one thread of a converged warp, 0 in the others.  The copy and MMA warps
+// run their loops as whole warps and predicate what one thread issues with it:
+// a branch around each issue, or a loop that one lane runs by itself, takes
+// longer, since these instructions take warp-uniform operands.
+__device__ __forceinline__ uint32_t elected() {
   uint32_t p;
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-  return p != 0;
+  return p;
+}
+
+__device__ __forceinline__ void arrive_if(uint32_t leader, uint32_t bar) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %1, 0;\n@p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar),
+               "r"(leader)
+               : "memory");
+}
+
+__device__ __forceinline__ void expect_if(uint32_t leader, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %2, 0;\n@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(
+          bar),
+      "r"(bytes), "r"(leader)
+      : "memory");
 }
 
 // Arrival on an mbarrier of the cluster (a shared::cluster address) without
 // memory ordering: what it orders is tensor memory, which the tcgen05 fences
 // around it and around the wait cover.  (With release at cluster scope it would
 // first wait for every load in flight: the scales fetched ahead.)
-__device__ __forceinline__ void arrive_cluster(uint32_t remote) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(remote) : "memory");
+__device__ __forceinline__ void arrive_cluster_if(uint32_t leader, uint32_t remote) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %1, 0;\n@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n}\n" ::
+          "r"(remote),
+      "r"(leader)
+      : "memory");
 }
 
 // Instruction word of tcgen05.mma kind::f8f6f4: float32 accumulator, both
 // operands e4m3 and K-major, an m x n tile.
 constexpr uint32_t mma_word(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
 
+// Blocks [z, z + U) of rows [y, ..) into this CTA's shared memory (out-of-range
+// ones read as zero), the bytes completing on an mbarrier of the cluster (a
+// pair's CTA 0).
+template <int CTAS>
+__device__ __forceinline__ void load_box(uint32_t leader, uint32_t dst, const void* map, int y, int z, uint32_t bar) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
+        "@p cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4}], [%5];\n}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar), "r"(leader)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
+        "@p cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar), "r"(leader)
+        : "memory");
+}
+
+// The MMA of one K = 32 step; `add` = 0 starts the accumulator afresh.
+template <int CTAS>
+__device__ __forceinline__ void issue_mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t word,
+                                          uint32_t add) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"(add), "r"(leader));
+  else
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"(add), "r"(leader));
+}
+
+// Arrives on the mbarrier (in both CTAs of a pair) once the MMAs issued before have completed.
+template <int CTAS>
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %2, 0;\n"
+        "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::
+            "r"(bar),
+        "h"(static_cast<uint16_t>(3)), "r"(leader)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %1, 0;\n"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(leader)
+        : "memory");
+}
+
 // The rows' tiles.  Group g's rows are cut into tiles of TM rows; `start` and
 // `first` hold each group's first row and first row tile (the last entries:
 // the end of the rows and the number of row tiles).
-template <int G>
 struct Groups {
-  int start[G + 1];
-  int first[G + 1];
+  int* start;  // [groups + 1] each, in shared memory
+  int* first;
 };
 
 // Fills `t` from the offsets (one warp), clamped to [0, rows] and to the
 // largest before them.
-template <int TM, int G>
-__device__ __forceinline__ void build_groups(Groups<G>& t, const int64_t* offsets, int groups, int64_t rows,
+template <int TM>
+__device__ __forceinline__ void build_groups(const Groups& t, const int64_t* offsets, int groups, int64_t rows,
                                              int lane) {
   auto clamped = [&](int i) -> int {
     const int64_t o = i <= groups ? offsets[i] : 0;
@@ -162,7 +223,9 @@ struct Tile {
 constexpr int kBand = 8;
 
 template <int TM>
-__device__ __forceinline__ Tile tile_at(int64_t tile, int groups, const int* start, const int* first, int wtiles) {
+__device__ __forceinline__ Tile tile_at(int64_t tile, int groups, const Groups& map, int wtiles) {
+  const int* const start = map.start;
+  const int* const first = map.first;
   const int slot = static_cast<int>(tile / wtiles);
   int lo = 0, hi = groups;  // first[lo] <= slot < first[hi]
   while (hi - lo > 1) {

@@ -16,30 +16,27 @@
 namespace {
 
 using bnn::fp8::Args;
-using bnn::tc::mbar_arrive;
-using bnn::tc::mbar_expect_tx;
-using bnn::tc::mma_commit;
 using bnn::tc::smem_u32;
 using bnn::tc::sw128_desc;
-using bnn::tc::tma_load_2d;
 using bnn::tc::tmem_ld16;
 using bnn::tc::tmem_wait_ld;
 
 // ---------------------------------------------------------------------------
-// Few rows: weights on the tensor-memory lanes.
+// Up to 32 rows (of a group): weights on the tensor-memory lanes.
 //
 // Tile: 128 weight rows (one scale block: the weight scale of a block of k is
 // one number for the CTA) x BN activation rows as the MMA's N, so a handful of
 // rows costs a handful of columns and the weights stream once at whatever rate
-// HBM gives.  Stages of one block of k (128 bytes a row, one 128-byte-swizzled
-// TMA box per operand).  When the tiles leave SMs idle, a cluster of KS CTAs
-// splits the blocks of k and adds its partial sums in rank order through
-// distributed shared memory: the order is fixed, so results are reproducible.
+// HBM gives.  A ring stage holds U blocks of k (one 3-D TMA box per operand);
+// each block has an accumulator of its own, two sets of U in tensor memory.
+// When the tiles leave SMs idle, a cluster of KS CTAs splits the blocks of k and
+// adds its partial sums in rank order through distributed shared memory: the
+// order is fixed, so results are reproducible.  Two CTAs share an SM.
 //
-// Roles: a TMA thread; an MMA thread; four epilogue warps, each 32 weight rows:
-// they read a block's BN sums (tcgen05.ld), scale and add them.  The scales of
-// the BN rows reach every lane through a per-warp line of shared memory, loaded
-// ahead from global memory (coalesced: the scale matrix is block-major).
+// Roles: four epilogue warps, each 32 weight rows (they read the accumulators,
+// scale and add); a TMA warp; an MMA warp; a scale warp, which writes the
+// products of the rows' scales and the weight block's to shared memory, ahead,
+// from where every lane reads all BN.
 //
 // Launched with programmatic dependent launch: the weights' first stages are
 // fetched before the wait for the kernel ahead (not for groups, whose tiles
@@ -48,19 +45,23 @@ using bnn::tc::tmem_wait_ld;
 constexpr int kTm = 128;                    // weight rows of a tile
 constexpr int kBlockBytes = 128;            // bytes of a row's block of k
 constexpr int kEpi = 128;                   // epilogue threads
-constexpr int kThreads = kEpi + 64;         // + TMA warp + MMA warp
-constexpr int kTmaWarp = kEpi / 32, kMmaWarp = kTmaWarp + 1;
-constexpr int kAhead = 4;                   // blocks whose activation scales are in flight
+constexpr int kTmaWarp = kEpi / 32, kMmaWarp = kTmaWarp + 1, kScaleWarp = kTmaWarp + 2;
+constexpr int kThreads = kEpi + 3 * 32;
+constexpr int U = 2;                        // blocks of k per iteration
+constexpr int kBufs = 2;                    // accumulator sets
+constexpr int kScaleSlots = 2 * kBufs;      // iterations whose scales are in shared memory
+constexpr int kScaleAhead = 2;              // iterations whose scales are in flight
 
 template <int BN>
 struct Cfg {
-  static constexpr uint32_t kStageBytes = (kTm + BN) * kBlockBytes;
-  static constexpr int kStages = 5;                                  // two CTAs an SM (up to 113 KiB each)
-  static constexpr int kBufs = 128 / BN;                               // accumulators in tensor memory
-  static constexpr uint32_t kTmemCols = BN * kBufs;                  // 128: two CTAs (and the next kernel's) fit the 512
+  static constexpr uint32_t kWBlock = kTm * kBlockBytes, kXBlock = BN * kBlockBytes;
+  static constexpr uint32_t kStageBytes = U * (kWBlock + kXBlock);
+  static constexpr int kStages = 110592 / kStageBytes;               // two CTAs an SM
+  static constexpr uint32_t kTmemCols = kBufs * U * BN;              // 64 or 128
   static constexpr size_t kSmem = kStages * kStageBytes + 1024;
+  static_assert(kXBlock % 1024 == 0, "swizzle atoms stay aligned");
+  static_assert(kStages >= kBufs && BN * kEpi * 4 <= kStages * kStageBytes, "the split's exchange fits the ring");
 };
-static_assert(Cfg<16>::kStageBytes % 1024 == 0 && Cfg<32>::kStageBytes % 1024 == 0, "swizzle atoms stay aligned");
 
 template <int BN, int KS, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -71,31 +72,32 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
   static_assert(KS == 1 || !GROUPED, "a split cluster takes one tile");
   namespace cg = cooperative_groups;
   using C = Cfg<BN>;
-  constexpr int S = C::kStages, NB = C::kBufs;
+  constexpr int S = C::kStages;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], part_full[NB], part_empty[NB];
+  __shared__ __align__(8) uint64_t full_bar[S], done_bar[S], scale_bar[kScaleSlots], free_bar[kBufs];
   __shared__ uint32_t tmem_holder;
   __shared__ int any_bad;
-  __shared__ __align__(16) float scales[4][2][BN];
-  __shared__ bnn::fp8::Groups<GROUPED ? BNN_MAX_GROUPS : 1> map;
+  __shared__ __align__(16) float scales[kScaleSlots][U][BN];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  // (behind the ring, as long as this call's groups: two CTAs share an SM's memory)
+  int* const group_map = reinterpret_cast<int*>(smem + S * C::kStageBytes);
+  const bnn::fp8::Groups map{group_map, group_map + groups + 1};
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(smem);
   const int rank = KS > 1 ? static_cast<int>(blockIdx.x % KS) : 0;
   const int wtiles = static_cast<int>((n + kTm - 1) / kTm);
-  const int b0 = static_cast<int>(static_cast<int64_t>(kb) * rank / KS);
-  const int b1 = static_cast<int>(static_cast<int64_t>(kb) * (rank + 1) / KS);
+  const int its = (kb + U - 1) / U;
+  const int i0 = static_cast<int>(static_cast<int64_t>(its) * rank / KS);
+  const int i1 = static_cast<int>(static_cast<int64_t>(its) * (rank + 1) / KS);
 
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       bnn::tc::mbar_init(smem_u32(&full_bar[i]), 1);
-      bnn::tc::mbar_init(smem_u32(&empty_bar[i]), 1);
+      bnn::tc::mbar_init(smem_u32(&done_bar[i]), 1);
     }
-    for (int i = 0; i < NB; ++i) {
-      bnn::tc::mbar_init(smem_u32(&part_full[i]), 1);
-      bnn::tc::mbar_init(smem_u32(&part_empty[i]), 4);
-    }
+    for (int i = 0; i < kScaleSlots; ++i) bnn::tc::mbar_init(smem_u32(&scale_bar[i]), 1);
+    for (int i = 0; i < kBufs; ++i) bnn::tc::mbar_init(smem_u32(&free_bar[i]), kEpi / 32);
     any_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -124,92 +126,115 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
   bnn::pdl_trigger();
   const int64_t tiles = static_cast<int64_t>(map.first[groups]) * wtiles;
   const int64_t step = gridDim.x / KS, tile0 = blockIdx.x / KS;
+  const uint32_t full = smem_u32(full_bar), done = smem_u32(done_bar), ready = smem_u32(scale_bar),
+                 freed = smem_u32(free_bar), leader = bnn::fp8::elected();
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ TMA copies
-    uint32_t it = 0;  // stages issued
+    bnn::fp8::Ring<S> st;
     bool ok = true, waited = GROUPED;
     for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
-      const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map.start, map.first, wtiles);
+      const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map, wtiles);
       const int wrow = t.group * static_cast<int>(n) + t.wtile * kTm;
-      int b = b0;
-      if (!waited) {  // the first stages' weights, then the wait, then their activations
-        const int ahead = min(S, b1 - b0);
-        for (int i = 0; i < ahead; ++i) {
-          if (bnn::fp8::elected()) {
-            mbar_expect_tx(smem_u32(&full_bar[i]), C::kStageBytes);
-            tma_load_2d(ring + i * C::kStageBytes, &tmap_w, (b0 + i) * kBlockBytes, wrow, smem_u32(&full_bar[i]));
-          }
-          __syncwarp();
+      int ahead = i0;  // the iteration up to which the weights are already on their way
+      if (!waited) {
+        ahead += min(S, i1 - i0);
+        for (int i = i0; i < ahead; ++i) {
+          bnn::fp8::expect_if(leader, full + 8 * (i - i0), C::kStageBytes);
+          bnn::fp8::load_box<1>(leader, ring + (i - i0) * C::kStageBytes, &tmap_w, wrow, i * U, full + 8 * (i - i0));
         }
         bnn::pdl_wait();
-        for (int i = 0; i < ahead; ++i) {
-          if (bnn::fp8::elected())
-            tma_load_2d(ring + i * C::kStageBytes + kTm * kBlockBytes, &tmap_x, (b0 + i) * kBlockBytes, t.row,
-                        smem_u32(&full_bar[i]));
-          __syncwarp();
-        }
-        b += ahead;
-        it = static_cast<uint32_t>(ahead);
         waited = true;
       }
-      for (; b < b1; ++b, ++it) {
-        const int st = static_cast<int>(it % S);
-        if (it >= static_cast<uint32_t>(S))
-          ok = bnn::fp8::wait(smem_u32(&empty_bar[st]), (it / S + 1) & 1u, errors);
-        ok = __all_sync(0xffffffffu, ok);
+      for (int i = i0; i < i1; ++i, st.next()) {
+        // (the round before a barrier's first counts as done)
+        ok = bnn::fp8::wait(done + 8 * st.at, st.round ^ 1u, errors);
         if (!ok) break;
-        if (bnn::fp8::elected()) {
-          const uint32_t dst = ring + st * C::kStageBytes, bar = smem_u32(&full_bar[st]);
-          mbar_expect_tx(bar, C::kStageBytes);
-          tma_load_2d(dst, &tmap_w, b * kBlockBytes, wrow, bar);
-          tma_load_2d(dst + kTm * kBlockBytes, &tmap_x, b * kBlockBytes, t.row, bar);
+        const uint32_t dst = ring + st.at * C::kStageBytes, bar = full + 8 * st.at;
+        if (i >= ahead) {
+          bnn::fp8::expect_if(leader, bar, C::kStageBytes);
+          bnn::fp8::load_box<1>(leader, dst, &tmap_w, wrow, i * U, bar);
         }
-        __syncwarp();
+        bnn::fp8::load_box<1>(leader, dst + U * C::kWBlock, &tmap_x, t.row, i * U, bar);
       }
     }
-    // the CTA must not retire with copies in flight
-    for (uint32_t c = it >= static_cast<uint32_t>(S) ? it - S : 0; c < it; ++c)
-      bnn::tc::mbar_drain(smem_u32(&full_bar[c % S]), (c / S) & 1u, errors);
-    if (KS > 1) {
-      __syncwarp();
-      cluster.sync();
-      cluster.sync();
-    }
+    if (!waited) bnn::pdl_wait();
+    // The CTA must not retire with copies in flight: every stage's last MMAs are waited for (they follow its copies).
+    for (int i = 0; i < S; ++i, st.next()) bnn::fp8::wait(done + 8 * st.at, st.round ^ 1u, errors);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     if (!GROUPED) bnn::pdl_wait();  // before the first bounded wait (for copies that start after it)
     constexpr uint32_t word = bnn::fp8::mma_word(kTm, BN);
-    uint32_t it = 0;
+    const uint64_t desc = sw128_desc(ring);
+    bnn::fp8::Ring<S> st;
+    bnn::fp8::Ring<kBufs> acc;
     bool ok = true;
     for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
-      for (int b = b0; b < b1; ++b, ++it) {
-        const int st = static_cast<int>(it % S), pb = static_cast<int>(it % NB);
-        if (it >= static_cast<uint32_t>(NB))
-          ok = bnn::fp8::wait(smem_u32(&part_empty[pb]), (it / NB + 1) & 1u, errors);
-        if (ok) ok = bnn::fp8::wait(smem_u32(&full_bar[st]), (it / S) & 1u, errors);
-        ok = __all_sync(0xffffffffu, ok);
+      for (int i = i0; i < i1; ++i, st.next(), acc.next()) {
+        ok = bnn::fp8::wait2(freed + 8 * acc.at, acc.round ^ 1u, full + 8 * st.at, st.round, errors);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-        if (bnn::fp8::elected()) {
-          const uint64_t ad = sw128_desc(ring + st * C::kStageBytes);
-          const uint64_t bd = sw128_desc(ring + st * C::kStageBytes + kTm * kBlockBytes);
+        const uint64_t ad = desc + st.at * (C::kStageBytes >> 4), bd = ad + (U * C::kWBlock >> 4);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            asm volatile(
-                "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem + pb * BN),
-                "l"(ad + static_cast<uint64_t>(2 * kk)), "l"(bd + static_cast<uint64_t>(2 * kk)), "r"(word),
-                "r"(kk > 0 ? 1u : 0u));
-          mma_commit(smem_u32(&empty_bar[st]));
-          mma_commit(smem_u32(&part_full[pb]));
-        }
-        __syncwarp();
+            bnn::fp8::issue_mma<1>(leader, tmem + acc.at * (U * BN) + u * BN, ad + (u * (C::kWBlock >> 4) + 2 * kk),
+                                   bd + (u * (C::kXBlock >> 4) + 2 * kk), word, kk > 0 ? 1u : 0u);
+        bnn::fp8::commit<1>(leader, done + 8 * st.at);
       }
     }
-    // every MMA issued has completed before the CTA's memory is given back
-    for (uint32_t c = it >= static_cast<uint32_t>(S) ? it - S : 0; c < it; ++c)
-      bnn::tc::mbar_drain(smem_u32(&empty_bar[c % S]), (c / S) & 1u, errors);
+  } else if (warp == kScaleWarp) {
+    // ------------------------------------------------------------ scales
+    if (!GROUPED) bnn::pdl_wait();  // the activation scales may come from the preceding kernel
+    bnn::fp8::Ring<kScaleSlots> sl;
+    bnn::fp8::Ring<kBufs> old;
+    bool ok = true;
+    int lead = kBufs;
+    for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+      const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map, wtiles);
+      const bool live = lane < BN && lane < t.end - t.row;
+      const float* wsp = ws + (static_cast<int64_t>(t.group) * wtiles + t.wtile) * kb;
+      const float* xsp = xs + t.row + lane;
+      float x[kScaleAhead][U], w[kScaleAhead][U];
+      auto load = [&](int i, int a) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int b = i * U + u;
+          x[a][u] = b < kb && i < i1 && live ? __ldg(xsp + b * rows) : 0.0f;
+          w[a][u] = b < kb && i < i1 ? __ldg(wsp + b) : 0.0f;
+        }
+      };
+#pragma unroll
+      for (int a = 0; a < kScaleAhead; ++a) load(i0 + a, a);
+      for (int i = i0; i < i1 && ok; i += kScaleAhead) {
+#pragma unroll
+        for (int a = 0; a < kScaleAhead; ++a) {
+          if (i + a < i1 && ok) {
+            // Before an iteration's scales are written, those of kScaleSlots before must have been read: it waits
+            // until the accumulators of kBufs before have been.  That barrier's next phase is this iteration's,
+            // which needs these scales, so the phase cannot be missed.
+            if (lead > 0) {
+              --lead;
+            } else {
+              ok = bnn::fp8::wait(freed + 8 * old.at, old.round, errors);
+              old.next();
+            }
+            if (ok) {
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+                if (lane < BN) scales[sl.at][u][lane] = x[a][u] * w[a][u];
+              load(i + a + kScaleAhead, a);
+              __syncwarp();
+              bnn::fp8::arrive_if(leader, ready + 8 * sl.at);
+              sl.next();
+            }
+          }
+        }
+      }
+    }
+  }
+  if (warp >= kEpi / 32) {
     if (KS > 1) {
       __syncwarp();
       cluster.sync();
@@ -217,66 +242,39 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
     }
   } else {
     // ------------------------------------------------------------ scale and add
-    if (!GROUPED) bnn::pdl_wait();  // the activation scales may come from the preceding kernel
-    constexpr int PL = (BN + 31) / 32;  // rows' scales a lane loads per block
-    uint32_t it = 0;
+    if (!GROUPED) bnn::pdl_wait();
+    const uint32_t src0 = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    bnn::fp8::Ring<S> st;
+    bnn::fp8::Ring<kScaleSlots> sl;
+    uint32_t buf = 0;
     bool ok = true;
-    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
-    const int64_t nb = wtiles;
     for (int64_t tile = tile0; tile < tiles; tile += step) {
-      const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map.start, map.first, wtiles);
-      const float* wsp = ws + (t.group * nb + t.wtile) * kb;
+      const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map, wtiles);
       const int live = min(BN, t.end - t.row);
       float acc[BN];
 #pragma unroll
       for (int c = 0; c < BN; ++c) acc[c] = 0.0f;
-      // both scales of the blocks ahead, multiplied when used: a product here would wait for its loads
-      float px[kAhead][PL], pw[kAhead];
-      auto load = [&](int b, int a) {
-        pw[a] = b < b1 ? __ldg(wsp + b) : 0.0f;
+      for (int i = i0; i < i1; ++i, st.next(), sl.next(), buf ^= 1u) {
+        ok = bnn::fp8::wait2(done + 8 * st.at, st.round, ready + 8 * sl.at, sl.round, errors);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+        uint32_t r[U * BN / 16][16];
 #pragma unroll
-        for (int p = 0; p < PL; ++p) {
-          const int c = lane + 32 * p;
-          px[a][p] = b < b1 && c < live ? __ldg(xs + b * rows + t.row + c) : 0.0f;
-        }
-      };
+        for (int c = 0; c < U * BN / 16; ++c) tmem_ld16(src0 + buf * (U * BN) + 16 * c, r[c]);
+        tmem_wait_ld();
+        asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+        float4 s[U * BN / 4];
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) load(b0 + a, a);
-      for (int b = b0; b < b1 && ok; b += kAhead) {
+        for (int c = 0; c < U * BN / 4; ++c) s[c] = reinterpret_cast<const float4*>(&scales[sl.at][0][0])[c];
+        bnn::fp8::arrive_if(leader, freed + 8 * buf);  // accumulators and scales are in this warp's registers
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-          if (b + a < b1 && ok) {
-            float* line = scales[warp][a & 1];
-#pragma unroll
-            for (int p = 0; p < PL; ++p)
-              if (lane + 32 * p < BN) line[lane + 32 * p] = px[a][p] * pw[a];
-            load(b + a + kAhead, a);
-            const int pb = static_cast<int>(it % NB);
-            ok = bnn::fp8::wait(smem_u32(&part_full[pb]), (it / NB) & 1u, errors);
-            ok = __all_sync(0xffffffffu, ok);
-            __syncwarp();  // every lane's part of `line` is written
-            if (ok) {
-              asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-#pragma unroll
-              for (int c0 = 0; c0 < BN; c0 += 16) {
-                uint32_t r[16];
-                tmem_ld16(tmem + lanes + pb * BN + c0, r);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 16; c += 4) {
-                  const float4 s = *reinterpret_cast<const float4*>(line + c0 + c);
-                  acc[c0 + c] = fmaf(__uint_as_float(r[c]), s.x, acc[c0 + c]);
-                  acc[c0 + c + 1] = fmaf(__uint_as_float(r[c + 1]), s.y, acc[c0 + c + 1]);
-                  acc[c0 + c + 2] = fmaf(__uint_as_float(r[c + 2]), s.z, acc[c0 + c + 2]);
-                  acc[c0 + c + 3] = fmaf(__uint_as_float(r[c + 3]), s.w, acc[c0 + c + 3]);
-                }
-              }
-              asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
-              __syncwarp();  // also orders this block's reads of `line` before its next writes
-              if (lane == 0) mbar_arrive(smem_u32(&part_empty[pb]));
-            }
-            ++it;
-          }
+        for (int c = 0; c < U * BN; c += 4) {
+          const float4 v = s[c / 4];
+          float* a = acc + c % BN;
+          a[0] = fmaf(__uint_as_float(r[c / 16][c % 16]), v.x, a[0]);
+          a[1] = fmaf(__uint_as_float(r[c / 16][c % 16 + 1]), v.y, a[1]);
+          a[2] = fmaf(__uint_as_float(r[c / 16][c % 16 + 2]), v.z, a[2]);
+          a[3] = fmaf(__uint_as_float(r[c / 16][c % 16 + 3]), v.w, a[3]);
         }
       }
       const int64_t j = static_cast<int64_t>(t.wtile) * kTm + tid;
@@ -346,21 +344,19 @@ bnn_status launch_narrow(const Args& a) {
   const int64_t rtiles = GROUPED ? a.rows / BN + (a.rows < a.groups ? a.rows : a.groups) : (a.rows + BN - 1) / BN;
   const int64_t tiles = rtiles * wtiles, slots = 2 * bnn::sm_count();
   const int64_t ctas = KS > 1 ? tiles * KS : (tiles < slots ? tiles : slots);
-  // grid limits, and stages counted in 32 bits
-  if (ctas > INT32_MAX || (tiles + slots - 1) / slots * a.kb >= (int64_t{1} << 31)) return BNN_ERR_INVALID_ARG;
+  if (ctas > INT32_MAX) return BNN_ERR_INVALID_ARG;
   CUtensorMap tw, tx;
-  const uint64_t pitch = static_cast<uint64_t>(a.kb) * kBlockBytes;
-  if (!bnn::encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq, pitch, static_cast<uint64_t>(a.groups * a.n),
-                           pitch, kBlockBytes, kTm, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !bnn::encode_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.xq, pitch, static_cast<uint64_t>(a.rows), pitch,
-                           kBlockBytes, BN, CU_TENSOR_MAP_SWIZZLE_128B))
+  const uint64_t kb = static_cast<uint64_t>(a.kb);
+  if (!bnn::encode_tmap_blocks(&tw, a.wq, static_cast<uint64_t>(a.groups * a.n), kb, kTm, U) ||
+      !bnn::encode_tmap_blocks(&tx, a.xq, static_cast<uint64_t>(a.rows), kb, BN, U))
     return BNN_ERR_UNSUPPORTED;
   unsigned int* errors = bnn::device_error_counter();
   if (!errors) return bnn::cuda_fail(cudaGetLastError());
   auto kern = fp8_narrow_kernel<BN, KS, GROUPED>;
-  BNN_TRY(bnn::ensure_smem(kern, Cfg<BN>::kSmem));
+  const size_t smem = Cfg<BN>::kSmem + 2 * sizeof(int) * (a.groups + 1);
+  BNN_TRY(bnn::ensure_smem(kern, Cfg<BN>::kSmem + 2 * sizeof(int) * (BNN_MAX_GROUPS + 1)));
   const cudaError_t e =
-      bnn::launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Cfg<BN>::kSmem, a.stream, KS, tw, tx,
+      bnn::launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), smem, a.stream, KS, tw, tx,
                       a.xs, a.ws, a.bias, a.offsets, a.groups, a.rows, a.n, a.kb, a.out, a.out_type, errors);
   if (e != cudaSuccess) return bnn::cuda_fail(e);
   return bnn::check_launch();

@@ -32,7 +32,6 @@
 namespace {
 
 using bnn::fp8::Args;
-using bnn::tc::mbar_expect_tx;
 using bnn::tc::smem_u32;
 using bnn::tc::sw128_desc;
 using bnn::tc::tmem_wait_ld;
@@ -65,56 +64,6 @@ struct Cfg {
   static_assert(kWBlock % 1024 == 0, "swizzle atoms stay aligned");
   static_assert(kScaleAhead % U == 0 && kStages >= 2, "");
 };
-
-// One box into this CTA's shared memory, its bytes completing on an mbarrier of
-// the cluster (a pair's CTA 0).
-__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* map, int y, int z, uint32_t bar0) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-      "%4}], [%5];\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar0)
-      : "memory");
-}
-
-// Blocks [z, z + U) of rows [y, ..): out-of-range ones read as zero.
-template <int CTAS>
-__device__ __forceinline__ void load_box(uint32_t dst, const void* map, int y, int z, uint32_t bar) {
-  if constexpr (CTAS == 2)
-    tma_load_pair(dst, map, y, z, bar);
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];\n" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-
-template <int CTAS>
-__device__ __forceinline__ void issue_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t word, uint32_t add) {
-  if constexpr (CTAS == 2)
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(word), "r"(add));
-  else
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(word), "r"(add));
-}
-
-// Arrives on the mbarrier (in both CTAs of a pair) once the MMAs issued before have completed.
-template <int CTAS>
-__device__ __forceinline__ void commit(uint32_t bar) {
-  if constexpr (CTAS == 2)
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
-            bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-  else
-    bnn::tc::mma_commit(bar);
-}
 
 template <int N>
 __device__ __forceinline__ void load_cols(uint32_t addr, uint32_t (&r)[N]) {
@@ -153,7 +102,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   __shared__ float scales[kScaleSlots][U][C::kHalves][kTm];
   __shared__ float stage_out[kEpiWarps][32][kStoreCols + 1];
   __shared__ uint32_t tmem_holder;
-  __shared__ bnn::fp8::Groups<GROUPED ? BNN_MAX_GROUPS : 1> map;
+  __shared__ int group_map[2][GROUPED ? BNN_MAX_GROUPS + 1 : 2];
+  const bnn::fp8::Groups map{group_map[0], group_map[1]};
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CTAS == 2 ? cg::this_cluster().block_rank() : 0;
@@ -204,7 +154,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
 
   if (warp >= kEpiWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kControlRegs));
-    const uint32_t full = smem_u32(full_bar), done = smem_u32(done_bar);
+    const uint32_t full = smem_u32(full_bar), done = smem_u32(done_bar), leader = bnn::fp8::elected();
     if (warp == kTmaWarp) {
       // ---------------------------------------------------------- TMA copies
       uint32_t full0 = full;  // a pair's: CTA 0's
@@ -212,37 +162,30 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       bnn::fp8::Ring<S> st;
       bool ok = true, waited = GROUPED;
       for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
-        const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map.start, map.first, wtiles);
+        const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map, wtiles);
         const int xrow = t.row + kTm * static_cast<int>(rank);
         const int wrow = t.group * static_cast<int>(n) + t.wtile * TN + C::kWRows * static_cast<int>(rank);
         int ahead = 0;  // stages whose weights are already on their way
         if (!waited) {
           ahead = min(S, its);
-          if (bnn::fp8::elected()) {
-            for (int i = 0; i < ahead; ++i) {
-              if (rank == 0) mbar_expect_tx(full + 8 * i, CTAS * C::kStageBytes);
-              load_box<CTAS>(ring + i * C::kStageBytes + C::kXBytes, &tmap_w, wrow, i * U, full0 + 8 * i);
-            }
+          for (int i = 0; i < ahead; ++i) {
+            if (rank == 0) bnn::fp8::expect_if(leader, full + 8 * i, CTAS * C::kStageBytes);
+            bnn::fp8::load_box<CTAS>(leader, ring + i * C::kStageBytes + C::kXBytes, &tmap_w, wrow, i * U, full0 + 8 * i);
           }
-          __syncwarp();
           bnn::pdl_wait();
           waited = true;
         }
         for (int b = 0; b < its; ++b, st.next()) {
           // (the round before a barrier's first counts as done)
           ok = bnn::fp8::wait(done + 8 * st.at, st.round ^ 1u, errors);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          if (bnn::fp8::elected()) {
-            const uint32_t dst = ring + st.at * C::kStageBytes, bar = full0 + 8 * st.at;
-            if (b >= ahead) {
-              if (rank == 0) mbar_expect_tx(full + 8 * st.at, CTAS * C::kStageBytes);
-              load_box<CTAS>(dst + C::kXBytes, &tmap_w, wrow, b * U, bar);
-            }
-            load_box<CTAS>(dst, &tmap_x, xrow, b * U, bar);
+          if (!ok) break;
+          const uint32_t dst = ring + st.at * C::kStageBytes, bar = full0 + 8 * st.at;
+          if (b >= ahead) {
+            if (rank == 0) bnn::fp8::expect_if(leader, full + 8 * st.at, CTAS * C::kStageBytes);
+            bnn::fp8::load_box<CTAS>(leader, dst + C::kXBytes, &tmap_w, wrow, b * U, bar);
           }
-          __syncwarp();
+          bnn::fp8::load_box<CTAS>(leader, dst, &tmap_x, xrow, b * U, bar);
         }
-        ok = __all_sync(0xffffffffu, ok);
       }
       if (!waited) bnn::pdl_wait();
       // The CTA must not retire with copies in flight: every stage's last MMAs are waited for (they follow its
@@ -260,22 +203,18 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
         for (int b = 0; b < its; ++b, st.next(), acc.next()) {
           ok = bnn::fp8::wait2(freed + 8 * acc.at, acc.round ^ 1u, full + 8 * st.at, st.round, errors);
-          if (!__all_sync(0xffffffffu, ok)) break;
+          if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-          if (bnn::fp8::elected()) {
-            const uint64_t ad = desc + st.at * (C::kStageBytes >> 4), bd = ad + (C::kXBytes >> 4);
-            const uint32_t d = tmem + acc.at * (U * TN);
+          const uint64_t ad = desc + st.at * (C::kStageBytes >> 4), bd = ad + (C::kXBytes >> 4);
+          const uint32_t d = tmem + acc.at * (U * TN);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                issue_mma<CTAS>(d + u * TN, ad + (u * (C::kXBlock >> 4) + 2 * kk), bd + (u * (C::kWBlock >> 4) + 2 * kk),
-                                word, kk > 0 ? 1u : 0u);
-            commit<CTAS>(done + 8 * st.at);
-          }
-          __syncwarp();
+            for (int kk = 0; kk < 4; ++kk)
+              bnn::fp8::issue_mma<CTAS>(leader, d + u * TN, ad + (u * (C::kXBlock >> 4) + 2 * kk),
+                              bd + (u * (C::kWBlock >> 4) + 2 * kk), word, kk > 0 ? 1u : 0u);
+          bnn::fp8::commit<CTAS>(leader, done + 8 * st.at);
         }
-        ok = __all_sync(0xffffffffu, ok);
       }
     } else if (warp >= kScaleWarp) {
       // ---------------------------------------------------------- scales
@@ -295,7 +234,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       bool ok = true;
       int lead = kBufs;
       for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
-        const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map.start, map.first, wtiles);
+        const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map, wtiles);
         const int row = t.row + kTm * static_cast<int>(rank) + r0;
         const int live = t.end - row, wb = t.wtile * TN / 128;
         const bool two = C::kHalves == 2 && wb + 1 < nb;
@@ -325,7 +264,6 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
                 ok = bnn::fp8::wait(read + 8 * old.at, old.round, errors);
                 old.next();
               }
-              ok = __all_sync(0xffffffffu, ok);
               if (ok) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -337,8 +275,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
                   load(a + u);
                 }
                 __syncwarp();
-                if (bnn::fp8::elected()) bnn::tc::mbar_arrive(ready + 8 * st.at);
-                __syncwarp();
+                bnn::fp8::arrive_if(leader, ready + 8 * st.at);
                 st.next();
               }
             }
@@ -355,16 +292,13 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
     const uint32_t done = smem_u32(done_bar), ready = smem_u32(scale_bar);
     uint32_t freed0 = smem_u32(free_bar);  // a pair's: CTA 0's
     if constexpr (CTAS == 2) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(freed0) : "r"(smem_u32(free_bar)));
-    auto release = [&](uint32_t buf) {  // this warp has the accumulator in registers
+    const uint32_t leader = bnn::fp8::elected();
+    auto release = [&](uint32_t buf) {  // this warp has the accumulators in registers (its loads are warp-wide)
       asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
-      __syncwarp();
-      if (bnn::fp8::elected()) {
-        if constexpr (CTAS == 2)
-          bnn::fp8::arrive_cluster(freed0 + 8 * buf);
-        else
-          bnn::tc::mbar_arrive(freed0 + 8 * buf);
-      }
-      __syncwarp();
+      if constexpr (CTAS == 2)
+        bnn::fp8::arrive_cluster_if(leader, freed0 + 8 * buf);
+      else
+        bnn::fp8::arrive_if(leader, freed0 + 8 * buf);
     };
     bnn::fp8::Ring<S> st;
     bnn::fp8::Ring<kScaleSlots> sl;
@@ -376,7 +310,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       for (int c = 0; c < CW / 2; ++c) acc[c] = 0;
       for (int b = 0; b < its; ++b, st.next(), sl.next(), buf ^= 1u) {
         ok = bnn::fp8::wait2(done + 8 * st.at, st.round, ready + 8 * sl.at, sl.round, errors);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
         const uint32_t src = src0 + buf * (U * TN);
         const float* sc = &scales[sl.at][0][C::kHalves == 2 ? part : 0][32 * q + lane];
@@ -399,10 +333,9 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
                  s[c0 / CW]);
         }
       }
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       // ---------------------------------------------------------- store
-      const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map.start, map.first, wtiles);
+      const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map, wtiles);
       const int64_t row0 = t.row + kTm * static_cast<int>(rank) + 32 * q;  // this warp's first row
       const int64_t j0 = static_cast<int64_t>(t.wtile) * TN + part * CW;
       const int live = static_cast<int>(min(int64_t{32}, t.end - row0));
