@@ -223,19 +223,18 @@ struct Tile {
 constexpr int kBand = 8;
 
 template <int TM>
-__device__ __forceinline__ Tile tile_at(int64_t tile, int groups, const Groups& map, int wtiles) {
+__device__ __forceinline__ Tile tile_at(int tile, int groups, const Groups& map, int wtiles) {
   const int* const start = map.start;
   const int* const first = map.first;
-  const int slot = static_cast<int>(tile / wtiles);
+  const int slot = tile / wtiles;
   int lo = 0, hi = groups;  // first[lo] <= slot < first[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (first[mid] <= slot) lo = mid; else hi = mid;
   }
   const int mt = first[lo + 1] - first[lo];
-  const int64_t local = tile - static_cast<int64_t>(first[lo]) * wtiles;
-  const int band = static_cast<int>(local / (static_cast<int64_t>(kBand) * wtiles));
-  const int r = static_cast<int>(local - static_cast<int64_t>(band) * kBand * wtiles);
+  const int local = tile - first[lo] * wtiles, band = local / (kBand * wtiles);
+  const int r = local - band * kBand * wtiles;
   const int height = min(kBand, mt - band * kBand);
   Tile t;
   t.group = lo;

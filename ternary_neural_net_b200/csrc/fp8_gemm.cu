@@ -124,8 +124,8 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
   asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
   const uint32_t tmem = tmem_holder;
   bnn::pdl_trigger();
-  const int64_t tiles = static_cast<int64_t>(map.first[groups]) * wtiles;
-  const int64_t step = gridDim.x / KS, tile0 = blockIdx.x / KS;
+  const int tiles = map.first[groups] * wtiles;  // (the launch keeps it within 32 bits)
+  const int step = gridDim.x / KS, tile0 = blockIdx.x / KS;
   const uint32_t full = smem_u32(full_bar), done = smem_u32(done_bar), ready = smem_u32(scale_bar),
                  freed = smem_u32(free_bar), leader = bnn::fp8::elected();
 
@@ -133,7 +133,7 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
     // ------------------------------------------------------------ TMA copies
     bnn::fp8::Ring<S> st;
     bool ok = true, waited = GROUPED;
-    for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+    for (int tile = tile0; tile < tiles && ok; tile += step) {
       const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map, wtiles);
       const int wrow = t.group * static_cast<int>(n) + t.wtile * kTm;
       int ahead = i0;  // the iteration up to which the weights are already on their way
@@ -169,7 +169,7 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
     bnn::fp8::Ring<S> st;
     bnn::fp8::Ring<kBufs> acc;
     bool ok = true;
-    for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+    for (int tile = tile0; tile < tiles && ok; tile += step) {
       for (int i = i0; i < i1; ++i, st.next(), acc.next()) {
         ok = bnn::fp8::wait2(freed + 8 * acc.at, acc.round ^ 1u, full + 8 * st.at, st.round, errors);
         if (!ok) break;
@@ -191,7 +191,7 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
     bnn::fp8::Ring<kBufs> old;
     bool ok = true;
     int lead = kBufs;
-    for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+    for (int tile = tile0; tile < tiles && ok; tile += step) {
       const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map, wtiles);
       const bool live = lane < BN && lane < t.end - t.row;
       const float* wsp = ws + (static_cast<int64_t>(t.group) * wtiles + t.wtile) * kb;
@@ -248,7 +248,7 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
     bnn::fp8::Ring<kScaleSlots> sl;
     uint32_t buf = 0;
     bool ok = true;
-    for (int64_t tile = tile0; tile < tiles; tile += step) {
+    for (int tile = tile0; tile < tiles; tile += step) {
       const bnn::fp8::Tile t = bnn::fp8::tile_at<BN>(tile, groups, map, wtiles);
       const int live = min(BN, t.end - t.row);
       float acc[BN];
@@ -344,7 +344,7 @@ bnn_status launch_narrow(const Args& a) {
   const int64_t rtiles = GROUPED ? a.rows / BN + (a.rows < a.groups ? a.rows : a.groups) : (a.rows + BN - 1) / BN;
   const int64_t tiles = rtiles * wtiles, slots = 2 * bnn::sm_count();
   const int64_t ctas = KS > 1 ? tiles * KS : (tiles < slots ? tiles : slots);
-  if (ctas > INT32_MAX) return BNN_ERR_INVALID_ARG;
+  if (ctas > INT32_MAX || tiles > INT32_MAX - slots) return BNN_ERR_INVALID_ARG;
   CUtensorMap tw, tx;
   const uint64_t kb = static_cast<uint64_t>(a.kb);
   if (!bnn::encode_tmap_blocks(&tw, a.wq, static_cast<uint64_t>(a.groups * a.n), kb, kTm, U) ||

@@ -43,7 +43,8 @@ constexpr int kScaleSlots = 4;                 // iterations whose scales are in
 constexpr int kBufs = 2;                       // accumulator sets
 constexpr int kEpiWarps = 8, kTmaWarp = kEpiWarps, kMmaWarp = kTmaWarp + 1, kScaleWarp = kTmaWarp + 2;
 constexpr int kThreads = 32 * (kEpiWarps + 4);
-constexpr int kStoreCols = 16;                 // columns per staged store step
+constexpr int kStoreCols = 16;                 // columns per step of an unaligned store
+constexpr int kStagePitch = 20;                // words per row of a warp's store staging (16-byte accesses without bank conflicts)
 // Registers a thread: 168 at launch (three warps in each SM sub-partition's 16384), of
 // which the control warpgroup keeps 72 and each epilogue warpgroup takes 216.
 constexpr int kControlRegs = 72, kEpiRegs = 216;
@@ -58,20 +59,12 @@ struct Cfg {
   static constexpr int kStages = 196608 / kStageBytes;              // 192 KiB of stages
   static constexpr uint32_t kTmemCols = kBufs * U * TN;             // 512
   static constexpr int kCols = TN / 2;                              // columns of an epilogue thread
-  static constexpr int kLoad = kCols < 32 || kCols > 64 ? 16 : 32;  // columns per load of tensor memory
+  static constexpr int kHold = kCols > 64 ? 3 : 4;                  // 16-column loads in flight per thread
   static constexpr int kHalves = TN > 128 ? 2 : 1;                  // weight scale blocks of a tile
   static constexpr size_t kSmem = kStages * kStageBytes + 1024;
   static_assert(kWBlock % 1024 == 0, "swizzle atoms stay aligned");
   static_assert(kScaleAhead % U == 0 && kStages >= 2, "");
 };
-
-template <int N>
-__device__ __forceinline__ void load_cols(uint32_t addr, uint32_t (&r)[N]) {
-  if constexpr (N == 16)
-    bnn::tc::tmem_ld16(addr, r);
-  else
-    bnn::tc::tmem_ld32(addr, r);
-}
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t v;
@@ -85,6 +78,56 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t s) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;\n" : "+l"(acc) : "l"(a), "l"(s));
 }
 
+// Two outputs as words of the output type.
+__device__ __forceinline__ void put2(uint32_t* w, float a, float b, float) {
+  w[0] = __float_as_uint(a);
+  w[1] = __float_as_uint(b);
+}
+__device__ __forceinline__ void put2(uint32_t* w, float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  w[0] = *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void put2(uint32_t* w, float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  w[0] = *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A warp's 32 rows (lane = row, CW columns each) to `out` (pitch n, 16-byte
+// aligned rows), the first `live` of them, in pieces of up to 64 bytes a row.
+template <int CW, typename T>
+__device__ __forceinline__ void store_rows(const uint64_t (&acc)[CW / 2], float* stage, T* out, const float* bias,
+                                           int64_t n, int live, int lane) {
+  constexpr int kCols = CW * sizeof(T) < 64 ? CW : 64 / static_cast<int>(sizeof(T));  // columns of a piece
+  constexpr int kWords = kCols * sizeof(T) / 4, kLanes = kWords / 4;                  // a lane stores 16 bytes
+#pragma unroll
+  for (int c = 0; c < CW; c += kCols) {
+    constexpr int kQuad = 16 / sizeof(T);  // columns of 16 bytes
+    __syncwarp();                          // the last piece has been read
+#pragma unroll
+    for (int i = 0; i < kCols; i += kQuad) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < kQuad; e += 2) {
+        float a, b;
+        unpack2(acc[(c + i + e) / 2], a, b);
+        if (bias) {
+          a += __ldg(bias + c + i + e);
+          b += __ldg(bias + c + i + e + 1);
+        }
+        put2(w + e * sizeof(T) / 4, a, b, T{});
+      }
+      *reinterpret_cast<uint4*>(stage + lane * kStagePitch + i * sizeof(T) / 4) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 32; r += 32 / kLanes) {
+      const int row = r + lane / kLanes, word = 4 * (lane % kLanes);
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + row * kStagePitch + word);
+      if (row < live) *reinterpret_cast<uint4*>(out + row * n + c + word * 4 / sizeof(T)) = v;
+    }
+  }
+}
+
 template <int CTAS, int TN, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 1)
 fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
@@ -93,14 +136,14 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
                 void* __restrict__ out, int out_type, int wide, unsigned int* errors) {
   namespace cg = cooperative_groups;
   using C = Cfg<CTAS, TN>;
-  constexpr int S = C::kStages, U = C::U, CW = C::kCols, LD = C::kLoad, kRows = CTAS * kTm;
+  constexpr int S = C::kStages, U = C::U, CW = C::kCols, H = C::kHold, kRows = CTAS * kTm;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[S];   // a pair: CTA 0's, for both CTAs' copies
   __shared__ __align__(8) uint64_t done_bar[S];   // the stage's MMAs: frees the stage, fills the accumulator
   __shared__ __align__(8) uint64_t scale_bar[kScaleSlots];  // the iteration's scales are in `scales`
   __shared__ __align__(8) uint64_t free_bar[kBufs];         // a pair: CTA 0's; one arrival per epilogue warp
   __shared__ float scales[kScaleSlots][U][C::kHalves][kTm];
-  __shared__ float stage_out[kEpiWarps][32][kStoreCols + 1];
+  __shared__ __align__(16) float stage_out[kEpiWarps][32 * kStagePitch];
   __shared__ uint32_t tmem_holder;
   __shared__ int group_map[2][GROUPED ? BNN_MAX_GROUPS + 1 : 2];
   const bnn::fp8::Groups map{group_map[0], group_map[1]};
@@ -149,8 +192,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
   const uint32_t tmem = tmem_holder;
   bnn::pdl_trigger();
-  const int64_t tiles = static_cast<int64_t>(map.first[groups]) * wtiles;
-  const int64_t step = gridDim.x / CTAS, tile0 = blockIdx.x / CTAS;
+  const int tiles = map.first[groups] * wtiles;  // (the launch keeps it within 32 bits)
+  const int step = gridDim.x / CTAS, tile0 = blockIdx.x / CTAS;
 
   if (warp >= kEpiWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kControlRegs));
@@ -161,7 +204,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       if constexpr (CTAS == 2) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(full0) : "r"(full));
       bnn::fp8::Ring<S> st;
       bool ok = true, waited = GROUPED;
-      for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+      for (int tile = tile0; tile < tiles && ok; tile += step) {
         const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map, wtiles);
         const int xrow = t.row + kTm * static_cast<int>(rank);
         const int wrow = t.group * static_cast<int>(n) + t.wtile * TN + C::kWRows * static_cast<int>(rank);
@@ -200,7 +243,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       bnn::fp8::Ring<S> st;
       bnn::fp8::Ring<kBufs> acc;
       bool ok = true;
-      for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+      for (int tile = tile0; tile < tiles && ok; tile += step) {
         for (int b = 0; b < its; ++b, st.next(), acc.next()) {
           ok = bnn::fp8::wait2(freed + 8 * acc.at, acc.round ^ 1u, full + 8 * st.at, st.round, errors);
           if (!ok) break;
@@ -233,7 +276,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       const uint32_t read = CTAS == 1 ? smem_u32(free_bar) : done;
       bool ok = true;
       int lead = kBufs;
-      for (int64_t tile = tile0; tile < tiles && ok; tile += step) {
+      for (int tile = tile0; tile < tiles && ok; tile += step) {
         const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map, wtiles);
         const int row = t.row + kTm * static_cast<int>(rank) + r0;
         const int live = t.end - row, wb = t.wtile * TN / 128;
@@ -304,7 +347,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
     bnn::fp8::Ring<kScaleSlots> sl;
     uint32_t buf = 0;
     bool ok = true;
-    for (int64_t tile = tile0; tile < tiles; tile += step) {
+    for (int tile = tile0; tile < tiles; tile += step) {
       uint64_t acc[CW / 2];
 #pragma unroll
       for (int c = 0; c < CW / 2; ++c) acc[c] = 0;
@@ -314,23 +357,27 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
         asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
         const uint32_t src = src0 + buf * (U * TN);
         const float* sc = &scales[sl.at][0][C::kHalves == 2 ? part : 0][32 * q + lane];
-        uint32_t r[2][LD];
-        load_cols<LD>(src, r[0]);
         uint64_t s[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) s[u] = pack2(sc[u * C::kHalves * kTm], sc[u * C::kHalves * kTm]);
+        // 16 columns a load, H loads in flight: a wait is for all of them, so each batch is followed by the loads
+        // of the next, issued as its registers fall free.
+        constexpr int kLoads = U * CW / 16;
+        uint32_t r[H][16];
+        auto fetch = [&](int c) { bnn::tc::tmem_ld16(src + c * 16 / CW * TN + c * 16 % CW, r[c % H]); };
 #pragma unroll
-        for (int c0 = 0; c0 < U * CW; c0 += LD) {  // LD columns at a time, the next ones on their way
-          const int i = (c0 / LD) & 1, next = c0 + LD, c = c0 % CW;
-          tmem_wait_ld();
-          if (next < U * CW)
-            load_cols<LD>(src + next / CW * TN + next % CW, r[i ^ 1]);
-          else
-            release(buf);
+        for (int c = 0; c < (H < kLoads ? H : kLoads); ++c) fetch(c);
 #pragma unroll
-          for (int j = 0; j < LD; j += 2)
-            fma2(acc[(c + j) / 2], pack2(__uint_as_float(r[i][j]), __uint_as_float(r[i][j + 1])),
-                 s[c0 / CW]);
+        for (int c = 0; c < kLoads; ++c) {
+          if (c % H == 0) {
+            tmem_wait_ld();
+            if (c + H >= kLoads) release(buf);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; j += 2)
+            fma2(acc[(c * 16 % CW + j) / 2], pack2(__uint_as_float(r[c % H][j]), __uint_as_float(r[c % H][j + 1])),
+                 s[c * 16 / CW]);
+          if (c + H < kLoads) fetch(c + H);
         }
       }
       if (!ok) break;
@@ -340,38 +387,51 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       const int64_t j0 = static_cast<int64_t>(t.wtile) * TN + part * CW;
       const int live = static_cast<int>(min(int64_t{32}, t.end - row0));
       if (live <= 0 || j0 >= n) continue;
+      float* const stage = stage_out[warp];
+      const float* const bj = bias ? bias + j0 : nullptr;
       if (wide && j0 + CW <= n) {
-        const int64_t at = (row0 + lane) * n + j0;
+        if constexpr (CW <= 64) {
+          // Pieces of 64 bytes a row through shared memory, so that a store instruction covers whole sectors of a
+          // few rows instead of 16 bytes of each of 32 (1024 x 11008 x 4096: 55.9 to 51.5 us).
+          if (out_type == BNN_TYPE_F32)
+            store_rows<CW, float>(acc, stage, static_cast<float*>(out) + row0 * n + j0, bj, n, live, lane);
+          else if (out_type == BNN_TYPE_BF16)
+            store_rows<CW, __nv_bfloat16>(acc, stage, static_cast<__nv_bfloat16*>(out) + row0 * n + j0, bj, n, live,
+                                          lane);
+          else
+            store_rows<CW, __half>(acc, stage, static_cast<__half*>(out) + row0 * n + j0, bj, n, live, lane);
+        } else {
+          // (128 accumulators a thread leave that path's registers no room: it spills inside the loop above, 541 us
+          // at 8192^3 against 481 with the rows stored directly.)
+          const int64_t at = (row0 + lane) * n + j0;
 #pragma unroll
-        for (int c = 0; c < CW; c += 8) {
-          float y[8];
+          for (int c = 0; c < CW; c += 8) {
+            float y[8];
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) unpack2(acc[(c + i) / 2], y[i], y[i + 1]);
-          if (bias) {
+            for (int i = 0; i < 8; i += 2) unpack2(acc[(c + i) / 2], y[i], y[i + 1]);
+            if (bias) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] += __ldg(bias + j0 + c + i);
+              for (int i = 0; i < 8; ++i) y[i] += __ldg(bj + c + i);
+            }
+            if (lane < live) bnn::fp8::store_eight(out, out_type, at + c, y);
           }
-          if (lane < live) bnn::fp8::store_eight(out, out_type, at + c, y);
         }
       } else {
-        // Rows whose starts 16-byte stores cannot take, or a tile that ends inside: a few columns at a time through
-        // shared memory, so that a warp stores a few rows' pieces side by side instead of 32 rows' single elements.
+        // Rows whose starts are not aligned, or a tile that ends inside: 16 columns at a time through shared memory,
+        // two rows' pieces an instruction.
 #pragma unroll
         for (int c = 0; c < CW; c += kStoreCols) {
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < kStoreCols; i += 2) {
-            float y0, y1;
-            unpack2(acc[(c + i) / 2], y0, y1);
-            stage_out[warp][lane][i] = y0;
-            stage_out[warp][lane][i + 1] = y1;
-          }
+          for (int i = 0; i < kStoreCols; i += 2)
+            unpack2(acc[(c + i) / 2], stage[lane * (kStoreCols + 1) + i], stage[lane * (kStoreCols + 1) + i + 1]);
           __syncwarp();
           const int64_t j = j0 + c + lane % kStoreCols;
-          const float bj = bias && j < n ? __ldg(bias + j) : 0.0f;
+          const float y0 = bias && j < n ? __ldg(bias + j) : 0.0f;
           if (j < n)
             for (int r = lane / kStoreCols; r < live; r += 32 / kStoreCols)
-              bnn::fp8::store_one(out, out_type, (row0 + r) * n + j, stage_out[warp][r][lane % kStoreCols] + bj);
+              bnn::fp8::store_one(out, out_type, (row0 + r) * n + j,
+                                  stage[r * (kStoreCols + 1) + lane % kStoreCols] + y0);
         }
       }
     }
@@ -399,6 +459,7 @@ bnn_status launch(const Args& a) {
       GROUPED ? a.rows / kRows + (a.rows < a.groups ? a.rows : a.groups) : (a.rows + kRows - 1) / kRows;
   const int64_t tiles = rtiles * wtiles, slots = bnn::sm_count() / CTAS;
   const int64_t units = tiles < slots ? tiles : slots;
+  if (tiles > INT32_MAX - slots) return BNN_ERR_INVALID_ARG;
   CUtensorMap tw, tx;
   const uint64_t kb = static_cast<uint64_t>(a.kb);
   if (!bnn::encode_tmap_blocks(&tw, a.wq, static_cast<uint64_t>(a.groups * a.n), kb, C::kWRows, C::U) ||
