@@ -216,11 +216,13 @@ __device__ __forceinline__ void build_groups(const Groups& t, const int64_t* off
 
 // Row tile and weight tile of tile index `tile`: the group's tiles run over up
 // to kBand row tiles before the next weight tile, so that the tiles at work at
-// one time share both their rows and their weights in L2.
+// one time share both their rows and their weights in L2 (8192^3: 250 MB read
+// from DRAM with bands of 16, 355 MB with bands of 8; 2048 x 8192 x 8192 in 140.0
+// and 141.7 us).
 struct Tile {
   int group, row, end, wtile;  // first row, end of the group's rows, weight tile
 };
-constexpr int kBand = 8;
+constexpr int kBand = 16;
 
 template <int TM>
 __device__ __forceinline__ Tile tile_at(int tile, int groups, const Groups& map, int wtiles) {

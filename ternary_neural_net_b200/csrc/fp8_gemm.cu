@@ -383,8 +383,8 @@ bnn_status gemm_tiles(const Args& a) {
     int ctas, tn;
     double block_us, store_us;
   };
-  static constexpr Shape kDense[] = {{1, 32, 0.156, 0.5}, {1, 64, 0.18, 1.0}, {1, 128, 0.26, 2.2}, {2, 256, 0.51, 3.0}};
-  static constexpr Shape kGrouped[] = {{1, 128, 0.26, 2.2}, {1, 256, 0.51, 3.0}, {2, 256, 0.51, 3.0}};
+  static constexpr Shape kDense[] = {{1, 32, 0.156, 0.4}, {1, 64, 0.19, 0.8}, {1, 128, 0.28, 1.2}, {2, 256, 0.51, 3.0}};
+  static constexpr Shape kGrouped[] = {{1, 128, 0.28, 1.2}, {1, 256, 0.51, 3.0}, {2, 256, 0.51, 3.0}};
   const bool grouped = a.offsets != nullptr;
   const Shape* shapes = grouped ? kGrouped : kDense;
   const int count = grouped ? 3 : 4;
@@ -407,16 +407,15 @@ bnn_status gemm_tiles(const Args& a) {
 }
 
 // Few rows (in the mean of the groups: their sizes are on the device): the
-// kernels that stream the weights.  Up to 8 rows and 2^26 bytes of weights the
-// register kernel (1 row, in us, against the tensor-memory one: 1024 x 1000 2.0
-// and 3.5, 4096 x 4096 5.6 and 6.5, 11008 x 4096 11.5 and 12.2, but 28672 x 8192
-// 54.7 and 41.4).  Above 32 rows the tile kernel (64 x 11008 x 4096: 14.3 us
-// against 16.7 with the weights on the lanes; but 32 x 4096 x 4096: 9.3 against
-// 7.7).
+// kernels that stream the weights.  Up to 8 rows and 2^25 bytes of weights the
+// register kernel (in us, against the tensor-memory one with 9 rows: 1024 x 1000
+// 2.0 and 3.4, 4096 x 4096 5.6 and 5.9, but 11008 x 4096 11.5 and 11.5, and 28672
+// x 8192 54.7 and 36.4).  Above 32 rows the tile kernel (64 x 11008 x 4096: 13.2
+// us; but 32 x 4096 x 4096 9.3 against 7.7).
 bnn_status dispatch(const Args& a) {
   if (a.kb == 0) return gemm_empty(a);
   const int64_t per = (a.rows + a.groups - 1) / a.groups;
-  if (!a.offsets && a.rows <= 8 && a.n * a.kb < (int64_t{1} << 19)) return bnn::fp8::gemm_skinny(a);
+  if (!a.offsets && a.rows <= 8 && a.n * a.kb <= (int64_t{1} << 18)) return bnn::fp8::gemm_skinny(a);
   if (per <= 16) return narrow<16>(a);
   if (per <= 32) return narrow<32>(a);
   return gemm_tiles(a);

@@ -12,12 +12,23 @@
 //
 // A ring stage holds U blocks of k (128 bytes a row each, one 3-D TMA box per
 // operand); each block's four MMAs of K = 32 start an accumulator of their own,
-// U x TN = 256 columns, two such sets in tensor memory.  While the epilogue
-// reads one set, scales it and adds it to its float32 registers, the tensor
-// cores fill the other.  What an iteration of a role costs is mostly the
-// latency of its hundred-odd dependent instructions (some 600 clocks measured
-// for the MMA warp and the copies alone), so narrow tiles take several blocks
-// per iteration.
+// U x TN = 256 columns (128 at TN = 32), two such sets in tensor memory.  While
+// the epilogue reads one set, scales it and adds it to its float32 registers,
+// the tensor cores fill the other.  What an iteration of a role costs is mostly
+// the latency of its hundred-odd dependent instructions (some 600 clocks
+// measured for the MMA warp and the copies alone), so narrow tiles take several
+// blocks per iteration (256 x 4096 x 4096 with TN = 64: 15.6 us with one, 10.8
+// with four).
+//
+// What bounds it.  A set is 512 clocks of MMAs.  TN = 128 moves 64 KiB per
+// iteration into the SM, 1024 clocks at the 64 bytes a clock that an SM reads
+// from L2, and takes 950-1000; a pair's 256 x 256 moves 32 KiB, and its epilogue
+// (128 columns a thread, two warps in each sub-partition: loads of tensor memory
+// and multiply-adds that wait for them) takes about 930.  That is 0.48 ms at
+// 8192^3 = 2280 TFLOP/s while the clock holds and 0.54 ms back to back under the
+// power cap.  Tried there: sixteen epilogue warps (0.55 ms), 32-column loads or
+// the next iteration's loads ahead of this one's end (0.51-0.58 ms: registers
+// spill), scalar multiply-adds (0.49 ms).
 //
 // Roles per CTA: warps 0-7 epilogue (lane quarter w % 4, column half w / 4),
 // warp 8 TMA, warp 9 MMA (CTA 0's issues for a pair), warps 10 and 11 the
