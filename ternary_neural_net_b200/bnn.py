@@ -389,52 +389,60 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _fp8_call(name, call, device, *args):
-    """call(*args, stream) with the operands' device current; tensors go as their pointers, None as NULL.
-    (A decoding step makes hundreds of these calls, each of a few microseconds on the GPU.)"""
-    index = device.index
+def _fp8_call(name, call, index, *args):
+    """call(*args, stream) with device `index` current; tensors go as their pointers, None as NULL.  (A decoding
+    step makes hundreds of these calls, each of a few microseconds on the GPU.)"""
     before = torch.cuda.current_device()
-    if before != index:
-        torch.cuda.set_device(index)
-    try:
+    if before == index:
         st = call(*args, _raw_stream(index))
-    finally:
-        if before != index:
+    else:
+        torch.cuda.set_device(index)
+        try:
+            st = call(*args, _raw_stream(index))
+        finally:
             torch.cuda.set_device(before)
     if st != BNN_OK:
         raise BnnError(st, name)
 
 
-def _same_device(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"operands are on {t.device} and {device}")
+_F8, _F32 = torch.float8_e4m3fn, torch.float32
 
 
-def _fp8_out(out, out_dtype, shape, device):
+def _is(t, dtype, index, shape):
+    """t is a contiguous tensor of this type and shape on CUDA device `index`."""
+    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()
+
+
+def _need(t, name, dtype, index, shape):
+    """Raises unless _is(t, ...): what _dev says of one tensor, then its device and shape."""
+    if _is(t, dtype, index, shape):
+        return
+    _dev(t, name, dtype, ndim=len(shape))
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the call on cuda:{index}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _fp8_out(out, out_dtype, shape, like, index):
     if out is None:
         if out_dtype not in TYPES:
             raise TypeError(f"out_dtype must be float32, bfloat16 or float16, got {out_dtype}")
-        return torch.empty(shape, dtype=out_dtype, device=device)
-    _dev(out, "out")
+        return like.new_empty(shape, dtype=out_dtype)
     if out.dtype not in TYPES:
         raise TypeError(f"out must be float32, bfloat16 or float16, got {out.dtype}")
-    if tuple(out.shape) != shape:
-        raise ValueError(f"out must have shape {shape}, got {tuple(out.shape)}")
+    _need(out, "out", out.dtype, index, shape)
     return out
 
 
-def _fp8_packed(q, scale, qshape, sshape, device):
+def _fp8_packed(q, scale, qshape, sshape, like, index):
     if q is None:
-        q = torch.empty(qshape, dtype=torch.float8_e4m3fn, device=device)
+        q = like.new_empty(qshape, dtype=_F8)
     else:
-        _dev(q, "q", torch.float8_e4m3fn, ndim=None)
+        _need(q, "q", _F8, index, qshape)
     if scale is None:
-        scale = torch.empty(sshape, dtype=torch.float32, device=device)
+        scale = like.new_empty(sshape, dtype=_F32)
     else:
-        _dev(scale, "scale", torch.float32, ndim=None)
-    if q.shape != qshape or scale.shape != sshape:
-        raise ValueError(f"q and scale must have shapes {qshape} and {sshape}")
+        _need(scale, "scale", _F32, index, sshape)
     return q, scale
 
 
@@ -446,16 +454,19 @@ def bnn_fp8_pack_rows(x: torch.Tensor, index: torch.Tensor | None = None, q: tor
     _dev(x, "x")
     if x.dtype not in TYPES:
         raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
+    dev = x.get_device()
     x_rows, k = x.shape
-    rows = x_rows
+    rows, ip = x_rows, None
     if index is not None:
-        _dev(index, "index", torch.int32, ndim=1)
+        if index.dim() != 1:
+            raise ValueError(f"index must be 1-D, got shape {tuple(index.shape)}")
         rows = index.shape[0]
-    kb = fp8_blocks(k)
-    q, scale = _fp8_packed(q, scale, (rows, 128 * kb), (kb, rows), x.device)
-    _same_device(x.device, index, q, scale)
-    _fp8_call("bnn_fp8_pack_rows", _lib.bnn_fp8_pack_rows, x.device, x.data_ptr(), TYPES[x.dtype], x_rows,
-              None if index is None else index.data_ptr(), rows, k, q.data_ptr(), scale.data_ptr())
+        _need(index, "index", torch.int32, dev, (rows,))
+        ip = index.data_ptr()
+    kb = (k + 127) // 128
+    q, scale = _fp8_packed(q, scale, (rows, 128 * kb), (kb, rows), x, dev)
+    _fp8_call("bnn_fp8_pack_rows", _lib.bnn_fp8_pack_rows, dev, x.data_ptr(), TYPES[x.dtype], x_rows, ip, rows, k,
+              q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -467,24 +478,26 @@ def bnn_fp8_pack_weight(w: torch.Tensor, q: torch.Tensor | None = None, scale: t
         raise TypeError(f"w must be float32, bfloat16 or float16, got {w.dtype}")
     if w.dim() not in (2, 3):
         raise ValueError(f"w must be [n, k] or [groups, n, k], got shape {tuple(w.shape)}")
+    dev = w.get_device()
     lead = tuple(w.shape[:-2])
     n, k = w.shape[-2:]
     groups = lead[0] if lead else 1
     kb = fp8_blocks(k)
-    q, scale = _fp8_packed(q, scale, (*lead, n, 128 * kb), (*lead, fp8_blocks(n), kb), w.device)
-    _same_device(w.device, q, scale)
-    _fp8_call("bnn_fp8_pack_weight", _lib.bnn_fp8_pack_weight, w.device, w.data_ptr(), TYPES[w.dtype], groups, n, k,
+    q, scale = _fp8_packed(q, scale, (*lead, n, 128 * kb), (*lead, fp8_blocks(n), kb), w, dev)
+    _fp8_call("bnn_fp8_pack_weight", _lib.bnn_fp8_pack_weight, dev, w.data_ptr(), TYPES[w.dtype], groups, n, k,
               q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
-def _fp8_activations(xq, xs):
-    _dev(xq, "xq", torch.float8_e4m3fn)
-    _dev(xs, "xs", torch.float32)
+def _fp8_rows(xq, xs):
+    """Checks packed activations [m, 128 kb] and [kb, m]: (device index, m, 128 kb)."""
+    _dev(xq, "xq", _F8)
+    dev = xq.get_device()
     m, kp = xq.shape
-    if kp % 128 or xs.shape != (kp // 128, m):
-        raise ValueError("xq must be [m, 128 kb] and xs [kb, m]")
-    return m, kp
+    if kp % 128:
+        raise ValueError(f"xq must be [m, 128 kb], got {tuple(xq.shape)}")
+    _need(xs, "xs", _F32, dev, (kp // 128, m))
+    return dev, m, kp
 
 
 def bnn_fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
@@ -492,20 +505,19 @@ def bnn_fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch
                  out: torch.Tensor | None = None) -> torch.Tensor:
     """Packed activations [m, k] x packed weights [n, k] -> [m, n] in out_dtype (out's type when out is
     given): scales applied, bias (float32 [n]) added."""
-    m, kp = _fp8_activations(xq, xs)
-    _dev(wq, "wq", torch.float8_e4m3fn)
-    _dev(ws, "ws", torch.float32)
+    dev, m, kp = _fp8_rows(xq, xs)
+    if wq.dim() != 2:
+        raise ValueError(f"wq must be [n, 128 kb], got {tuple(wq.shape)}")
     n = wq.shape[0]
-    if wq.shape[1] != kp or ws.shape != (fp8_blocks(n), kp // 128):
-        raise ValueError("wq must be [n, 128 kb] and ws [ceil(n/128), kb], with the kb of xq")
+    _need(wq, "wq", _F8, dev, (n, kp))
+    _need(ws, "ws", _F32, dev, ((n + 127) // 128, kp // 128))
+    bp = None
     if bias is not None:
-        _dev(bias, "bias", torch.float32, ndim=1)
-        if bias.shape[0] != n:
-            raise ValueError("bias must have n elements")
-    out = _fp8_out(out, out_dtype, (m, n), xq.device)
-    _same_device(xq.device, xs, wq, ws, bias, out)
-    _fp8_call("bnn_fp8_gemm", _lib.bnn_fp8_gemm, xq.device, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
-              None if bias is None else bias.data_ptr(), m, n, kp, out.data_ptr(), TYPES[out.dtype])
+        _need(bias, "bias", _F32, dev, (n,))
+        bp = bias.data_ptr()
+    out = _fp8_out(out, out_dtype, (m, n), xq, dev)
+    _fp8_call("bnn_fp8_gemm", _lib.bnn_fp8_gemm, dev, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), bp, m,
+              n, kp, out.data_ptr(), TYPES[out.dtype])
     return out
 
 
@@ -515,17 +527,14 @@ def bnn_fp8_grouped_gemm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, w
     """Rows offsets[g] <= i < offsets[g+1] of the packed activations [rows, k] x expert g of the packed
     weights [groups, n, k] -> [rows, n].  offsets int64 [groups + 1] stays on the device.  Rows outside
     every group are left as they are in `out` (uninitialised when `out` is not given)."""
-    rows, kp = _fp8_activations(xq, xs)
-    _dev(wq, "wq", torch.float8_e4m3fn, ndim=3)
-    _dev(ws, "ws", torch.float32, ndim=3)
-    _dev(offsets, "offsets", torch.int64, ndim=1)
+    dev, rows, kp = _fp8_rows(xq, xs)
+    if wq.dim() != 3:
+        raise ValueError(f"wq must be [groups, n, 128 kb], got {tuple(wq.shape)}")
     groups, n = wq.shape[0], wq.shape[1]
-    if wq.shape[2] != kp or ws.shape != (groups, fp8_blocks(n), kp // 128):
-        raise ValueError("wq must be [groups, n, 128 kb] and ws [groups, ceil(n/128), kb], with the kb of xq")
-    if offsets.shape[0] != groups + 1:
-        raise ValueError("offsets must have groups + 1 elements")
-    out = _fp8_out(out, out_dtype, (rows, n), xq.device)
-    _same_device(xq.device, xs, wq, ws, offsets, out)
-    _fp8_call("bnn_fp8_grouped_gemm", _lib.bnn_fp8_grouped_gemm, xq.device, xq.data_ptr(), xs.data_ptr(),
-              wq.data_ptr(), ws.data_ptr(), offsets.data_ptr(), groups, rows, n, kp, out.data_ptr(), TYPES[out.dtype])
+    _need(wq, "wq", _F8, dev, (groups, n, kp))
+    _need(ws, "ws", _F32, dev, (groups, (n + 127) // 128, kp // 128))
+    _need(offsets, "offsets", torch.int64, dev, (groups + 1,))
+    out = _fp8_out(out, out_dtype, (rows, n), xq, dev)
+    _fp8_call("bnn_fp8_grouped_gemm", _lib.bnn_fp8_grouped_gemm, dev, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(),
+              ws.data_ptr(), offsets.data_ptr(), groups, rows, n, kp, out.data_ptr(), TYPES[out.dtype])
     return out

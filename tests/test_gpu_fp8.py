@@ -534,3 +534,33 @@ def test_raw_tbin_layer_through_fp8(bnn):
     xq, xs = bnn.bnn_fp8_pack_rows(to_dev_f32(x))
     y, mag = fp8.gemm(*fp8.pack_rows(x), *[a[0] for a in fp8.pack_weight(w.astype(np.float32)[None])])
     assert_close(bnn.bnn_fp8_gemm(xq, xs, wq, ws), y, mag, 2, "f32", "raw layer")
+
+
+# ------------------------------------------------------------------------------------------ the binding's refusals
+def test_binding_refusals(bnn):
+    q = lambda *s: torch.zeros(s, device="cuda").to(torch.float8_e4m3fn)
+    f = lambda *s: torch.zeros(s, device="cuda")
+    xq, xs, wq, ws = q(4, 256), f(2, 4), q(130, 256), f(2, 2)
+    bad = [dict(xq=f(4, 256)), dict(xq=q(4, 200)), dict(xq=q(512, 8).t()), dict(xs=f(4, 2)), dict(xs=f(2, 4).double()),
+           dict(xs=f(4, 2).t()), dict(wq=q(130, 128)), dict(wq=q(1, 130, 256)), dict(ws=f(1, 2)), dict(ws=f(2, 2).cpu()),
+           dict(bias=f(129)), dict(bias=f(130).half()), dict(out_dtype=torch.float64), dict(out=f(4, 131)),
+           dict(out=f(4, 130).double()), dict(out=f(130, 4).t()), dict(out=torch.zeros(4, 130))]
+    for kw in bad:
+        with pytest.raises((TypeError, ValueError)):
+            bnn.bnn_fp8_gemm(**{**dict(xq=xq, xs=xs, wq=wq, ws=ws), **kw})
+    off = torch.zeros(4, dtype=torch.int64, device="cuda")
+    wq3, ws3 = q(3, 130, 256), f(3, 2, 2)
+    for kw in (dict(offsets=off[:3]), dict(offsets=off.int()), dict(offsets=off.cpu()), dict(wq=wq), dict(ws=ws),
+               dict(out=f(5, 130)), dict(offsets=off[None])):
+        with pytest.raises((TypeError, ValueError)):
+            bnn.bnn_fp8_grouped_gemm(**{**dict(xq=xq, xs=xs, wq=wq3, ws=ws3, offsets=off), **kw})
+    x = f(4, 200)
+    for kw in (dict(x=x.double()), dict(x=x[0]), dict(x=x.t()), dict(index=off), dict(index=off.int().cpu()),
+               dict(index=off.int()[None]), dict(q=q(4, 128)), dict(q=f(4, 256)), dict(scale=f(4, 2))):
+        with pytest.raises((TypeError, ValueError)):
+            bnn.bnn_fp8_pack_rows(**{**dict(x=x), **kw})
+    for kw in (dict(w=x.int()), dict(w=x[0]), dict(w=x[None, None]), dict(w=x.t()), dict(q=q(4, 128)),
+               dict(scale=f(2, 1))):
+        with pytest.raises((TypeError, ValueError)):
+            bnn.bnn_fp8_pack_weight(**{**dict(w=x), **kw})
+    assert bnn.bnn_fp8_gemm(xq, xs, wq, ws).shape == (4, 130)
