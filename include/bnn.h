@@ -49,9 +49,10 @@
  *     keep plain stream order.  So a weight operand must be complete before
  *     the stream reaches the matmuls that read it: after preparing it (with
  *     bnn_pack_signs, bnn_ternary_pack*, bnn_ternary_sparse_encode,
- *     bnn_tbin_load_ternary, bnn_fp8_pack_weight or any other kernel), synchronise the stream or
- *     the device, or prepare it on another stream and make this one wait on
- *     an event recorded there.  Activations packed or produced right before a
+ *     bnn_tbin_load_ternary or any other kernel), synchronise the stream or the
+ *     device, or prepare it on another stream and make this one wait on an
+ *     event recorded there.  (bnn_fp8_pack_weight needs neither on its own
+ *     stream; see there.)  Activations packed or produced right before a
  *     matmul on the same stream need nothing.
  */
 #ifndef BNN_H
@@ -465,6 +466,9 @@ bnn_status bnn_fp8_pack_rows(const void* x, int x_type, int64_t x_rows, const in
  *   scale   float32 [groups, ceil(n/128), kb], device.
  *   The rule of bnn_fp8_pack_rows with the maximum over the block's 128 x 128
  *   elements (fewer at the edges).
+ *   A second, empty kernel follows the pack on the stream, so matmuls enqueued
+ *   after this call on the same stream may read q and scale with nothing in
+ *   between (an exception to "Weights are static data").
  */
 bnn_status bnn_fp8_pack_weight(const void* w, int w_type, int64_t groups, int64_t n, int64_t k, uint8_t* q,
                                float* scale, cudaStream_t s);
@@ -482,6 +486,10 @@ bnn_status bnn_fp8_pack_weight(const void* w, int w_type, int64_t groups, int64_
  *   the sizes alone decide (results are bitwise reproducible), and there is one
  *   rounding to out_type.  Finite results need xs * ws finite in float32.
  *   wq and ws are weights in the sense of "Weights are static data" above.
+ *   The kernel is chosen by the sizes: up to 8 rows and 2^25 bytes of weights
+ *   from registers (mma.sync), up to 32 rows with the weights on the tensor-
+ *   memory lanes, above that tiles of 128 x 32..128 or a CTA pair's 256 x 256
+ *   (tcgen05).  No call allocates or keeps device memory.
  */
 bnn_status bnn_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const float* bias,
                         int64_t m, int64_t n, int64_t k, void* out, int out_type, cudaStream_t s);
@@ -501,7 +509,9 @@ bnn_status bnn_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, c
  *   out      [rows, n] of out_type, device: rows before offsets[0] and from
  *            offsets[groups] on are left as they were.
  *   Sums and rounding as for bnn_fp8_gemm; wq and ws are weights in the sense
- *   of "Weights are static data" (the offsets are not).
+ *   of "Weights are static data" (the offsets are not).  The kernel is chosen by
+ *   rows / groups, so a call whose groups differ much in size is answered as
+ *   correctly but suits one kernel less.
  */
 bnn_status bnn_fp8_grouped_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                                 const int64_t* offsets, int64_t groups, int64_t rows, int64_t n, int64_t k, void* out,
