@@ -199,6 +199,7 @@ fp8_pack_weight_kernel(const T* __restrict__ w, int64_t n, int64_t k, int64_t kb
   const int64_t t = blockIdx.x / col_tiles, j0 = (t % nb) * 128, g = t / nb;
   const int64_t b0 = (blockIdx.x % col_tiles) * L::kBlocks, e = b0 * 128 + lane * L::E;
   const int64_t row0 = j0 + warp * kRows;
+  bnn::pdl_trigger();  // (for the settle kernel, which waits for this one's end)
   const T* base = w + g * n * k;
   Words v[kRows];
 #pragma unroll
@@ -230,7 +231,7 @@ fp8_pack_weight_kernel(const T* __restrict__ w, int64_t n, int64_t k, int64_t kb
 }
 
 // Launched after the weight pack: see bnn_fp8_pack_weight.
-__global__ void fp8_settle_kernel() {}
+__global__ void fp8_settle_kernel() { bnn::pdl_wait(); }
 
 // The widest vector that the row pitch and the base allow, in elements.
 template <typename T>
@@ -271,7 +272,10 @@ bnn_status launch_weight(const T* w, int64_t groups, int64_t n, int64_t k, uint8
   const int64_t grid = groups * nb * col_tiles;
   if (grid > INT32_MAX) return BNN_ERR_INVALID_ARG;
   fp8_pack_weight_kernel<T, V><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(w, n, k, kb, nb, col_tiles, q, scale);
-  fp8_settle_kernel<<<1, 1, 0, s>>>();
+  const bnn_status st = bnn::check_launch();
+  if (st != BNN_OK) return st;
+  const cudaError_t e = bnn::launch_pdl(fp8_settle_kernel, dim3(1), dim3(1), 0, s, 1u);
+  if (e != cudaSuccess) return bnn::cuda_fail(e);
   return bnn::check_launch();
 }
 
@@ -305,10 +309,11 @@ extern "C" bnn_status bnn_fp8_pack_rows(const void* x, int x_type, int64_t x_row
   }
 }
 
-// The empty kernel behind the pack is an ordinary launch: it starts when the
-// pack is complete and visible, and a matmul launched with programmatic
-// dependent launch cannot start before it.  So weights packed here may be read
-// by the next matmul on the stream with nothing in between.
+// The kernel behind the pack waits until the pack is complete and visible and
+// then ends, without letting its successor start earlier.  A matmul launched
+// with programmatic dependent launch starts after that end at the earliest, so
+// weights packed here may be read by the next matmul on the stream with nothing
+// in between.
 extern "C" bnn_status bnn_fp8_pack_weight(const void* w, int w_type, int64_t groups, int64_t n, int64_t k, uint8_t* q,
                                           float* scale, cudaStream_t s) {
   if (w_type < BNN_TYPE_F32 || w_type > BNN_TYPE_F16 || groups < 0 || n < 0 || k < 0 || groups > BNN_MAX_GROUPS ||
