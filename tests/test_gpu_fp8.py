@@ -564,3 +564,95 @@ def test_binding_refusals(bnn):
         with pytest.raises((TypeError, ValueError)):
             bnn.bnn_fp8_pack_weight(**{**dict(w=x), **kw})
     assert bnn.bnn_fp8_gemm(xq, xs, wq, ws).shape == (4, 130)
+
+
+# ------------------------------------------------------------------------------------------ calls in other orders
+@pytest.mark.parametrize("m", [1, 20, 300])
+def test_weights_packed_inside_a_graph(bnn, m):
+    """A captured graph that packs weights and rows and multiplies them, replayed right behind the copies of its
+    next inputs: every replay's products are those of its own weights."""
+    n, k, g = 700, 1300, 3
+    ws_ = [to_dev_f32(synth.normal_f32(i, 6, (g, n, k))) for i in range(4)]
+    xs_ = [to_dev_f32(activations(i + 9, m, k)) for i in range(4)]
+    w, x = torch.empty((g, n, k), device="cuda"), torch.empty((m, k), device="cuda")
+    off = torch.tensor([0, m // 3, m // 3, m], device="cuda")
+
+    def call():
+        q, s = bnn.bnn_fp8_pack_weight(w)
+        xq, xs = bnn.bnn_fp8_pack_rows(x)
+        q2, s2 = bnn.bnn_fp8_pack_weight(w[1])
+        return bnn.bnn_fp8_gemm(xq, xs, q2, s2), bnn.bnn_fp8_grouped_gemm(xq, xs, q, s, off)
+    want = []
+    for i in range(4):
+        w.copy_(ws_[i]), x.copy_(xs_[i])
+        torch.cuda.synchronize()
+        want.append(call())
+        torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call()
+    got = []
+    for rep in range(3):
+        for i in range(4):
+            w.copy_(ws_[i]), x.copy_(xs_[i])
+            graph.replay()
+            got.append((i, outs[0].clone(), outs[1].clone()))
+    torch.cuda.synchronize()
+    for i, y, z in got:
+        assert torch.equal(y, want[i][0]) and torch.equal(z, want[i][1])
+    assert bnn.device_error_count() == 0
+
+
+@pytest.mark.parametrize("groups,rows", [(64, 900), (64, 2500), (8, 1500)])
+@pytest.mark.parametrize("place", [0, -1])
+def test_grouped_all_rows_in_one_group(bnn, groups, rows, place):
+    """The kernel is chosen by the mean size; here one group has every row and the others none."""
+    n, k = 300, 520
+    sizes = [0] * groups
+    sizes[place] = rows
+    xq, xs, wq, ws = packed_case(rows + groups, rows, n, k, groups)
+    offsets = offsets_of(sizes)
+    y, mag, live = fp8.grouped_gemm(xq, xs, wq, ws, offsets)
+    assert live.all()
+    got = bnn.bnn_fp8_grouped_gemm(*on_dev(xq, xs, wq, ws), torch.from_numpy(offsets).cuda())
+    assert_close(got, y, mag, fp8.blocks(k), "f32", f"{groups} {rows} {place}")
+
+
+def test_calls_from_several_threads(bnn):
+    """Host threads that pack and multiply at the same time, each on a stream of its own."""
+    import threading
+    shapes = [(1, 1000, 2000), (24, 700, 1100), (300, 900, 1000), (900, 1500, 640)]
+    data = [(to_dev_f32(activations(i, m, k)), to_dev_f32(synth.normal_f32(i, 7, (n, k))))
+            for i, (m, n, k) in enumerate(shapes)]
+
+    def call(x, w):
+        return bnn.bnn_fp8_gemm(*bnn.bnn_fp8_pack_rows(x), *bnn.bnn_fp8_pack_weight(w))
+    want = [call(*d) for d in data]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                ys = [call(*data[i]) for _ in range(20)]
+                torch.cuda.current_stream().synchronize()
+                wrong.extend(i for y in ys if not torch.equal(y, want[i]))
+        except Exception as e:  # noqa: BLE001 (reported by the main thread)
+            wrong.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(data))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+@pytest.mark.parametrize("m", [1, 9, 40, 300])
+def test_scales_far_apart(bnn, m):
+    """Scales near both ends of float32 whose products are ordinary numbers."""
+    n, k = 260, 900
+    xq, xs, wq, ws = packed_case(m, m, n, k)
+    xs = (xs * np.float32(2.0 ** -100)).astype(np.float32)
+    ws = (ws * np.float32(2.0 ** 110)).astype(np.float32)
+    y, mag = fp8.gemm(xq, xs, wq, ws)
+    assert_close(bnn.bnn_fp8_gemm(*on_dev(xq, xs, wq, ws)), y, mag, fp8.blocks(k), "f32", f"{m}")
