@@ -28,7 +28,9 @@
 // 8192^3 = 2280 TFLOP/s while the clock holds and 0.54 ms back to back under the
 // power cap.  Tried there: sixteen epilogue warps (0.55 ms), 32-column loads or
 // the next iteration's loads ahead of this one's end (0.51-0.58 ms: registers
-// spill), scalar multiply-adds (0.49 ms).
+// spill), scalar multiply-adds (0.49 ms), 256 x 192 tiles (0.53-0.59 ms, the same
+// with four loads in flight and with six: the epilogue takes some 2.9 clocks a
+// column and 220 a block whatever is in flight).
 //
 // Roles per CTA: warps 0-7 epilogue (lane quarter w % 4, column half w / 4),
 // warp 8 TMA, warp 9 MMA (CTA 0's issues for a pair), warps 10 and 11 the
