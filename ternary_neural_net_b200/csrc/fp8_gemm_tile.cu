@@ -415,7 +415,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
             store_rows<CW, __half>(acc, stage, static_cast<__half*>(out) + row0 * n + j0, bj, n, live, lane);
         } else {
           // (128 accumulators a thread leave that path's registers no room: it spills inside the loop above, 541 us
-          // at 8192^3 against 481 with the rows stored directly.)
+          // at 8192^3 against 481 with the rows stored directly.  16-byte units exchanged between the lanes of a quad
+          // instead of shared memory spill less and take 590.)
           const int64_t at = (row0 + lane) * n + j0;
 #pragma unroll
           for (int c = 0; c < CW; c += 8) {
