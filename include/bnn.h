@@ -490,7 +490,7 @@ bnn_status bnn_fp8_pack_weight(const void* w, int w_type, int64_t groups, int64_
  *   The kernel is chosen by the sizes: up to 8 rows and 2^25 bytes of weights
  *   from registers (mma.sync), up to 32 rows with the weights on the tensor-
  *   memory lanes, above that tiles of 128 x 32..128 or a CTA pair's 256 x 256
- *   (tcgen05).  No call allocates or keeps device memory.
+ *   (tcgen05; groups: 128 x 128 or 128 x 256).  No call allocates or keeps device memory.
  */
 bnn_status bnn_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const float* bias,
                         int64_t m, int64_t n, int64_t k, void* out, int out_type, cudaStream_t s);

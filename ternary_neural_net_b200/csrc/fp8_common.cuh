@@ -29,7 +29,8 @@ struct Args {
 
 // Up to 8 rows, one group.
 bnn_status gemm_skinny(const Args& a);
-// Tiles of 128 (ctas = 1) or 256 rows (a CTA pair) x tn columns.
+// Tiles of 128 rows (ctas = 1) x 32, 64 or 128 columns, or of 256 rows (a CTA
+// pair) x 256; for groups of 128 rows x 128 or 256.
 bnn_status gemm_tile(const Args& a, int ctas, int tn);
 
 // Bounded wait of a whole converged warp for an mbarrier phase: up to kPolls

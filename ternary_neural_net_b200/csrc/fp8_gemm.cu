@@ -380,19 +380,21 @@ bnn_status narrow(const Args& a) {
 // The tile kernel's shape for `rows` rows in `groups` groups: least modelled
 // time, waves x (blocks of k x us a block + us a store), of the shapes that a
 // sweep over 64 .. 8192 rows x 4096 .. 11008 x 4096 (and 8192^3) left; the model
-// is within about 10% of what it chooses between.  Groups: 128-row tiles (a
-// pair's 256 rows end inside groups of a few hundred: 522 us against 416 at 64
-// groups, 16384 rows x 4096 x 4096) unless the groups are long.
+// is within about 10% of what it chooses between.  Groups: 128-row tiles, 128 or
+// 256 columns wide (x 4096 x 4096: 8192 rows in 2 groups 158 and 148 us, 16384
+// rows in 64 groups 406 and 404).  A pair's 256 rows end inside the groups (423
+// us there, and 100 against 84 at 4096 rows in 8 groups); in groups of 2048 rows
+// they would save 2%, which is not worth a kernel.
 bnn_status gemm_tiles(const Args& a) {
   struct Shape {
     int ctas, tn;
     double block_us, store_us;
   };
   static constexpr Shape kDense[] = {{1, 32, 0.156, 0.4}, {1, 64, 0.19, 0.8}, {1, 128, 0.28, 1.2}, {2, 256, 0.51, 3.0}};
-  static constexpr Shape kGrouped[] = {{1, 128, 0.28, 1.2}, {1, 256, 0.51, 3.0}, {2, 256, 0.51, 3.0}};
+  static constexpr Shape kGrouped[] = {{1, 128, 0.28, 1.2}, {1, 256, 0.51, 3.0}};
   const bool grouped = a.offsets != nullptr;
   const Shape* shapes = grouped ? kGrouped : kDense;
-  const int count = grouped ? 3 : 4;
+  const int count = grouped ? 2 : 4;
   const int64_t sms = bnn::sm_count(), busy = a.rows < a.groups ? a.rows : a.groups;
   const Shape* best = shapes;
   double best_us = 0.0;

@@ -498,12 +498,9 @@ namespace bnn {
 namespace fp8 {
 
 bnn_status gemm_tile(const Args& a, int ctas, int tn) {
-  if (a.offsets) {
-    if (ctas == 2) return launch<2, 256, true>(a);
-    return tn == 256 ? launch<1, 256, true>(a) : launch<1, 128, true>(a);
-  }
+  if (a.offsets) return tn == 256 ? launch<1, 256, true>(a) : launch<1, 128, true>(a);
   if (ctas == 2) return launch<2, 256, false>(a);
-  return tn == 256 ? launch<1, 256, false>(a) : tn == 128 ? launch<1, 128, false>(a) : tn == 32 ? launch<1, 32, false>(a) : launch<1, 64, false>(a);
+  return tn == 128 ? launch<1, 128, false>(a) : tn == 64 ? launch<1, 64, false>(a) : launch<1, 32, false>(a);
 }
 
 }  // namespace fp8
