@@ -52,11 +52,15 @@ bnn_status bnn_probe_stream_read(const void* buf, int64_t bytes, int64_t blocks,
 /*
  * bnn_probe_wait_limit -- bound, in polls, the main mbarrier waits of the
  * tensor-core binary GEMM kernels (bnn_binary_gemm for m >= 64,
- * BNN_ALGO_TC, bnn_binary_linear) launched after this call; 0 restores the
- * normal bound (suspending polls for up to one second of wall time).  The
+ * BNN_ALGO_TC, bnn_binary_linear) and of the tcgen05 e4m3 kernels
+ * (bnn_fp8_grouped_gemm, bnn_fp8_gemm but for the register kernel of up to 8
+ * rows) launched after this call; 0 restores the normal bound (suspending
+ * polls: up to one second of wall time, e4m3 2^20 of them).  The e4m3 kernels'
+ * limited polls do not suspend.  The
  * final waits for copies and MMAs already in flight keep the normal bound
  * whatever the setting.  A wait that runs out
- * makes its CTA skip every store, wait for its copies and MMAs, free its
+ * makes its CTA skip every store (e4m3: every store of a tile whose sums it
+ * missed), wait for its copies and MMAs, free its
  * tensor memory and return; bnn_device_error_count() counts it.  With a
  * small limit (a few polls) the first waits run out before the first copies
  * land, which is how a test exercises that path without any GPU fault.

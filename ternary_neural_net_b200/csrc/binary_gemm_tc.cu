@@ -1077,6 +1077,8 @@ unsigned int* device_error_counter() {
   return g_counter[dev].ptr;
 }
 
+uint32_t wait_limit() { return g_wait_limit.load(); }
+
 }  // namespace bnn
 
 extern "C" int bnn_device_error_count(int reset) {

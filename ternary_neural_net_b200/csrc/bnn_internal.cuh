@@ -104,6 +104,9 @@ bnn_status binary_gemm_tc(const uint64_t* xp, const uint64_t* wp, const float* a
 // nullptr when the lookup fails.
 unsigned int* device_error_counter();
 
+// The bound that bnn_probe_wait_limit set, in polls; 0: the kernels' own.
+uint32_t wait_limit();
+
 // Bounded waits that ran out in the ternary tensor-core kernel (reset != 0 clears).
 int ternary_tc_error_count(int reset);
 

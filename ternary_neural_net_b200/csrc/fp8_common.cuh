@@ -33,31 +33,53 @@ bnn_status gemm_skinny(const Args& a);
 // pair) x 256; for groups of 128 rows x 128 or 256.
 bnn_status gemm_tile(const Args& a, int ctas, int tn);
 
-// Bounded wait of a whole converged warp for an mbarrier phase: up to kPolls
-// polls, each a try_wait and a vote, so that the branch is uniform.  (A wait on
+// Bounded wait of a whole converged warp for an mbarrier phase: up to `polls`
+// polls, each with a vote, so that the branch is uniform.  (A wait on
 // a completed phase takes some 70 clocks like this and about 130 as a loop that
 // each lane leaves by itself; bnn::tc::mbar_wait, which bounds by the wall
 // clock, takes longer still, and polls with a time hint wake hundreds of clocks
 // late.  These kernels wait twice per block of k and role.)  Every thread has
 // waited for the kernel ahead before its first call, so only copies and MMAs of
-// this kernel are waited for: microseconds, against 30 ms of polls at the least.
+// this kernel are waited for: microseconds, against 30 ms for kPolls polls at the
+// least.  The roles' waits take the launch's bound (kPolls, or less for a test:
+// bnn_probe_wait_limit), the drains always kPolls.
 // False, for the whole warp, when it ran out: counted in *errors by each thread.
 constexpr uint32_t kPolls = 1u << 20;
 
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, unsigned int* errors) {
+// The bound of a launch's waits.
+inline uint32_t main_polls() {
+  const uint32_t limit = wait_limit();
+  return limit && limit < kPolls ? limit : kPolls;
+}
+
+// One poll: try_wait, which suspends the warp for a while, or under a test's
+// bound test_wait, which returns at once.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t polls) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.eq.u32 q, %3, %4;\n"
+      "@q mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "@!q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(polls), "n"(kPolls)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t polls, unsigned int* errors) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < kPolls; ++i)
-    if (__all_sync(0xffffffffu, tc::mbar_try(bar, parity))) return true;
+  for (uint32_t i = polls; i != 0; --i)
+    if (__all_sync(0xffffffffu, poll(bar, parity, polls))) return true;
   atomicAdd(errors, 1u);
   return false;
 }
 
 // The same for two barriers at once: the polls' latencies overlap.
 __device__ __forceinline__ bool wait2(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b,
-                                      unsigned int* errors) {
+                                      uint32_t polls, unsigned int* errors) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < kPolls; ++i) {
-    const bool a = tc::mbar_try(bar_a, parity_a), b = tc::mbar_try(bar_b, parity_b);
+  for (uint32_t i = polls; i != 0; --i) {
+    const bool a = poll(bar_a, parity_a, polls), b = poll(bar_b, parity_b, polls);
     if (__all_sync(0xffffffffu, a && b)) return true;
   }
   atomicAdd(errors, 1u);
@@ -75,6 +97,17 @@ struct Ring {
     }
   }
 };
+
+// Waits for the newest phase of every slot of a ring whose next position is `st`
+// (a slot not used yet counts as done).  A CTA must not retire with copies or
+// MMAs in flight, whatever its roles' waits came to: so the copies are waited for
+// on their own barriers (MMAs that were never issued complete no others), and the
+// MMAs on the barriers of their commits.
+template <int N>
+__device__ __forceinline__ void drain(uint32_t bars, Ring<N> st, unsigned int* errors) {
+#pragma unroll 1
+  for (int i = 0; i < N; ++i, st.next()) wait(bars + 8 * st.at, st.round ^ 1u, kPolls, errors);
+}
 
 // 1 in one thread of a converged warp, 0 in the others.  The copy and MMA warps
 // run their loops as whole warps and predicate what one thread issues with it:
@@ -96,6 +129,15 @@ __device__ __forceinline__ void expect_if(uint32_t leader, uint32_t bar, uint32_
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.u32 p, %2, 0;\n@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(
           bar),
+      "r"(bytes), "r"(leader)
+      : "memory");
+}
+
+// `bytes` that no copy will bring count as landed.
+__device__ __forceinline__ void complete_if(uint32_t leader, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %2, 0;\n@p mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n}\n" ::
+          "r"(bar),
       "r"(bytes), "r"(leader)
       : "memory");
 }

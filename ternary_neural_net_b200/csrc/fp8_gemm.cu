@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
                   const float* __restrict__ xs, const float* __restrict__ ws, const float* __restrict__ bias,
                   const int64_t* __restrict__ offsets, int groups, int64_t rows, int64_t n, int kb,
-                  void* __restrict__ out, int out_type, unsigned int* errors) {
+                  void* __restrict__ out, int out_type, uint32_t polls, unsigned int* errors) {
   static_assert(KS == 1 || !GROUPED, "a split cluster takes one tile");
   namespace cg = cooperative_groups;
   using C = Cfg<BN>;
@@ -153,7 +153,7 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
       }
       for (int i = i0; i < i1; ++i, st.next()) {
         // (the round before a barrier's first counts as done)
-        ok = bnn::fp8::wait(done + 8 * st.at, st.round ^ 1u, errors);
+        ok = bnn::fp8::wait(done + 8 * st.at, st.round ^ 1u, polls, errors);
         if (!ok) break;
         const uint32_t dst = ring + st.at * C::kStageBytes, bar = full + 8 * st.at;
         if (i >= ahead) {
@@ -164,8 +164,7 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
       }
     }
     if (!waited) bnn::pdl_wait();
-    // The CTA must not retire with copies in flight: every stage's last MMAs are waited for (they follow its copies).
-    for (int i = 0; i < S; ++i, st.next()) bnn::fp8::wait(done + 8 * st.at, st.round ^ 1u, errors);
+    bnn::fp8::drain(full, st, errors);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     if (!GROUPED) bnn::pdl_wait();  // before the first bounded wait (for copies that start after it)
@@ -176,7 +175,7 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
     bool ok = true;
     for (int tile = tile0; tile < tiles && ok; tile += step) {
       for (int i = i0; i < i1; ++i, st.next(), acc.next()) {
-        ok = bnn::fp8::wait2(freed + 8 * acc.at, acc.round ^ 1u, full + 8 * st.at, st.round, errors);
+        ok = bnn::fp8::wait2(freed + 8 * acc.at, acc.round ^ 1u, full + 8 * st.at, st.round, polls, errors);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
         const uint64_t ad = desc + st.at * (C::kStageBytes >> 4), bd = ad + (U * C::kWBlock >> 4);
@@ -189,6 +188,7 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
         bnn::fp8::commit<1>(leader, done + 8 * st.at);
       }
     }
+    bnn::fp8::drain(done, st, errors);
   } else if (warp == kScaleWarp) {
     // ------------------------------------------------------------ scales
     if (!GROUPED) bnn::pdl_wait();  // the activation scales may come from the preceding kernel
@@ -222,7 +222,7 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
             if (lead > 0) {
               --lead;
             } else {
-              ok = bnn::fp8::wait(freed + 8 * old.at, old.round, errors);
+              ok = bnn::fp8::wait(freed + 8 * old.at, old.round, polls, errors);
               old.next();
             }
             if (ok) {
@@ -260,7 +260,7 @@ fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_const
 #pragma unroll
       for (int c = 0; c < BN; ++c) acc[c] = 0.0f;
       for (int i = i0; i < i1; ++i, st.next(), sl.next(), buf ^= 1u) {
-        ok = bnn::fp8::wait2(done + 8 * st.at, st.round, ready + 8 * sl.at, sl.round, errors);
+        ok = bnn::fp8::wait2(done + 8 * st.at, st.round, ready + 8 * sl.at, sl.round, polls, errors);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
         uint32_t r[U * BN / 16][16];
@@ -362,7 +362,8 @@ bnn_status launch_narrow(const Args& a) {
   BNN_TRY(bnn::ensure_smem(kern, Cfg<BN>::kSmem + 2 * sizeof(int) * (BNN_MAX_GROUPS + 1)));
   const cudaError_t e =
       bnn::launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), smem, a.stream, KS, tw, tx,
-                      a.xs, a.ws, a.bias, a.offsets, a.groups, a.rows, a.n, a.kb, a.out, a.out_type, errors);
+                      a.xs, a.ws, a.bias, a.offsets, a.groups, a.rows, a.n, a.kb, a.out, a.out_type,
+                      bnn::fp8::main_polls(), errors);
   if (e != cudaSuccess) return bnn::cuda_fail(e);
   return bnn::check_launch();
 }

@@ -37,7 +37,8 @@
 // scales: they multiply the rows' with the weight blocks' into shared memory,
 // ahead.  A pair's copies complete on CTA 0's barriers.  Every wait is bounded;
 // a role whose wait runs out stops (and with it, by their own bounds, those
-// that wait for it), and the outputs are unspecified.
+// that wait for it), and the outputs are unspecified.  Whatever the waits came
+// to, no CTA leaves before its copies and MMAs have completed.
 #include <cooperative_groups.h>
 
 #include "fp8_common.cuh"
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
                 const float* __restrict__ xs, const float* __restrict__ ws, const float* __restrict__ bias,
                 const int64_t* __restrict__ offsets, int groups, int64_t rows, int64_t n, int kb,
-                void* __restrict__ out, int out_type, int wide, unsigned int* errors) {
+                void* __restrict__ out, int out_type, int wide, uint32_t polls, unsigned int* errors) {
   namespace cg = cooperative_groups;
   using C = Cfg<CTAS, TN>;
   constexpr int S = C::kStages, U = C::U, CW = C::kCols, H = C::kHold, kRows = CTAS * kTm;
@@ -158,6 +159,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   __shared__ float scales[kScaleSlots][U][C::kHalves][kTm];
   __shared__ __align__(16) float stage_out[kEpiWarps][32 * kStagePitch];
   __shared__ uint32_t tmem_holder;
+  __shared__ uint32_t issued[2];            // a pair's CTA 0: how many stages' copies either CTA issued
+  __shared__ uint32_t tail_at, tail_round;  // and the ring's position behind them; CTA 1: behind the MMAs issued
   __shared__ int group_map[2][GROUPED ? BNN_MAX_GROUPS + 1 : 2];
   const bnn::fp8::Groups map{group_map[0], group_map[1]};
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -216,6 +219,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       uint32_t full0 = full;  // a pair's: CTA 0's
       if constexpr (CTAS == 2) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(full0) : "r"(full));
       bnn::fp8::Ring<S> st;
+      uint32_t count = 0;  // stages whose copies this CTA issued
       bool ok = true, waited = GROUPED;
       for (int tile = tile0; tile < tiles && ok; tile += step) {
         const bnn::fp8::Tile t = bnn::fp8::tile_at<kRows>(tile, groups, map, wtiles);
@@ -231,9 +235,9 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
           bnn::pdl_wait();
           waited = true;
         }
-        for (int b = 0; b < its; ++b, st.next()) {
+        for (int b = 0; b < its; ++b, ++count, st.next()) {
           // (the round before a barrier's first counts as done)
-          ok = bnn::fp8::wait(done + 8 * st.at, st.round ^ 1u, errors);
+          ok = bnn::fp8::wait(done + 8 * st.at, st.round ^ 1u, polls, errors);
           if (!ok) break;
           const uint32_t dst = ring + st.at * C::kStageBytes, bar = full0 + 8 * st.at;
           if (b >= ahead) {
@@ -244,9 +248,12 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
         }
       }
       if (!waited) bnn::pdl_wait();
-      // The CTA must not retire with copies in flight: every stage's last MMAs are waited for (they follow its
-      // copies).
-      for (int i = 0; i < S; ++i, st.next()) bnn::fp8::wait(done + 8 * st.at, st.round ^ 1u, errors);
+      if constexpr (CTAS == 1) {
+        bnn::fp8::drain(full, st, errors);
+      } else if (leader) {  // CTA 0 waits for both CTAs' copies, below
+        *cg::this_cluster().map_shared_rank(&issued[rank], 0) = count;
+        if (rank == 0) tail_at = st.at, tail_round = st.round;
+      }
     } else if (warp == kMmaWarp && rank == 0) {
       // ---------------------------------------------------------- MMA issue
       if (!GROUPED) bnn::pdl_wait();  // before the first bounded wait (for copies that start after it)
@@ -258,7 +265,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += step) {
         for (int b = 0; b < its; ++b, st.next(), acc.next()) {
-          ok = bnn::fp8::wait2(freed + 8 * acc.at, acc.round ^ 1u, full + 8 * st.at, st.round, errors);
+          ok = bnn::fp8::wait2(freed + 8 * acc.at, acc.round ^ 1u, full + 8 * st.at, st.round, polls, errors);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
           const uint64_t ad = desc + st.at * (C::kStageBytes >> 4), bd = ad + (C::kXBytes >> 4);
@@ -270,6 +277,13 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
               bnn::fp8::issue_mma<CTAS>(leader, d + u * TN, ad + (u * (C::kXBlock >> 4) + 2 * kk),
                               bd + (u * (C::kWBlock >> 4) + 2 * kk), word, kk > 0 ? 1u : 0u);
           bnn::fp8::commit<CTAS>(leader, done + 8 * st.at);
+        }
+      }
+      bnn::fp8::drain(done, st, errors);
+      if constexpr (CTAS == 2) {
+        if (leader) {
+          *cg::this_cluster().map_shared_rank(&tail_at, 1) = st.at;
+          *cg::this_cluster().map_shared_rank(&tail_round, 1) = st.round;
         }
       }
     } else if (warp >= kScaleWarp) {
@@ -317,7 +331,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
               if (lead > 0) {
                 --lead;
               } else {
-                ok = bnn::fp8::wait(read + 8 * old.at, old.round, errors);
+                ok = bnn::fp8::wait(read + 8 * old.at, old.round, polls, errors);
                 old.next();
               }
               if (ok) {
@@ -365,7 +379,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
 #pragma unroll
       for (int c = 0; c < CW / 2; ++c) acc[c] = 0;
       for (int b = 0; b < its; ++b, st.next(), sl.next(), buf ^= 1u) {
-        ok = bnn::fp8::wait2(done + 8 * st.at, st.round, ready + 8 * sl.at, sl.round, errors);
+        ok = bnn::fp8::wait2(done + 8 * st.at, st.round, ready + 8 * sl.at, sl.round, polls, errors);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
         const uint32_t src = src0 + buf * (U * TN);
@@ -454,6 +468,25 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constan
   asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
   __syncthreads();
   if constexpr (CTAS == 2) {
+    cg::this_cluster().sync();  // the roles of both CTAs have ended
+    // What is in flight is waited for where it completes: both CTAs' copies in CTA 0, and the commits' arrivals in
+    // CTA 1 (CTA 0's MMA warp has seen its own).  A stage's barrier expects both CTAs' bytes.  Where a wait ran out,
+    // one CTA may have issued up to S stages more than the other: CTA 0's account of those is set right first.
+    bnn::fp8::Ring<S> st;
+    st.at = tail_at, st.round = tail_round;
+    if (warp == kTmaWarp && rank == 0) {
+      const uint32_t full = smem_u32(full_bar), leader = bnn::fp8::elected();
+      const int more = static_cast<int>(issued[1] - issued[0]);  // CTA 1's stages that CTA 0 did not come to
+#pragma unroll 1
+      for (int i = 0; i < S; ++i, st.next()) {
+        const uint32_t bar = full + 8 * st.at;
+        if (i < more) bnn::fp8::expect_if(leader, bar, C::kStageBytes);
+        if (i >= S + more) bnn::fp8::complete_if(leader, bar, C::kStageBytes);
+        bnn::fp8::wait(bar, i < more ? st.round : st.round ^ 1u, bnn::fp8::kPolls, errors);
+      }
+    }
+    if (warp == kMmaWarp && rank == 1) bnn::fp8::drain(smem_u32(done_bar), st, errors);
+    __syncwarp();
     cg::this_cluster().sync();  // neither CTA leaves while the pair's tensor memory or barriers are in use
     if (warp == kMmaWarp)
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::kTmemCols));
@@ -487,7 +520,7 @@ bnn_status launch(const Args& a) {
   BNN_TRY(bnn::ensure_smem(kern, C::kSmem));
   const cudaError_t e = bnn::launch_pdl(kern, dim3(static_cast<unsigned>(CTAS * units)), dim3(kThreads), C::kSmem,
                                         a.stream, CTAS, tw, tx, a.xs, a.ws, a.bias, a.offsets, a.groups, a.rows, a.n,
-                                        a.kb, a.out, a.out_type, wide, errors);
+                                        a.kb, a.out, a.out_type, wide, bnn::fp8::main_polls(), errors);
   if (e != cudaSuccess) return bnn::cuda_fail(e);
   return bnn::check_launch();
 }
