@@ -483,9 +483,10 @@ bnn_status bnn_fp8_pack_weight(const void* w, int w_type, int64_t groups, int64_
  *     out[i,j] = round(sum_b xs[b,i] ws[j/128,b] sum_{e in block b} xq[i,e] wq[j,e] + bias[j]).
  *   The products are exact, each block's sum is taken in float32 by the tensor
  *   cores, the blocks' sums are scaled and added in float32 in an order that
- *   the sizes alone decide (results are bitwise reproducible), and there is one
- *   rounding to out_type.  The scales are multiplied first, in float32: results
- *   need xs * ws finite, and lose bits where it is below 2^-126.
+ *   the sizes and the device's number of SMs decide (results are bitwise
+ *   reproducible on one kind of device), and there is one rounding to out_type.
+ *   The scales are multiplied first, in float32: results need xs * ws finite,
+ *   and lose bits where it is below 2^-126.
  *   wq and ws are weights in the sense of "Weights are static data" above.
  *   The kernel is chosen by the sizes: up to 8 rows and 2^25 bytes of weights
  *   from registers (mma.sync), up to 32 rows with the weights on the tensor-

@@ -84,6 +84,21 @@ bnn_status bnn_probe_wait_limit(uint32_t polls);
  */
 bnn_status bnn_probe_ternary_plan(int64_t n, int64_t k, const int* active, int* rows, int* ks);
 
+/*
+ * bnn_probe_fp8_plan -- the kernel that bnn_fp8_gemm (groups = 0) or
+ * bnn_fp8_grouped_gemm (groups >= 1) uses for these sizes on a device of `sms`
+ * SMs (2 at least):
+ *   kernel     host out: 0 no k (bias or zeros), 1 the register kernel, 2 the
+ *              weights on the tensor-memory lanes, 3 activation rows on them;
+ *   tile_rows  host out: activation rows of a tile (3: 128, or 256 on a CTA pair);
+ *   tile_cols  host out: weight rows of a tile;
+ *   split      host out: CTAs per cluster splitting k.
+ * Host only, no CUDA call; BNN_ERR_INVALID_ARG for bad arguments.  A
+ * diagnostic of this library (no counterpart on the pages).
+ */
+bnn_status bnn_probe_fp8_plan(int64_t rows, int64_t n, int64_t k, int64_t groups, int sms, int* kernel,
+                              int* tile_rows, int* tile_cols, int* split);
+
 #ifdef __cplusplus
 }
 #endif

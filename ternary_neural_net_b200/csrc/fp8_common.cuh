@@ -27,6 +27,15 @@ struct Args {
   cudaStream_t stream;
 };
 
+// The kernel of a call: the product's rows and columns of a tile, and the CTAs
+// that split k.  Host only; sms: the device's SM count.
+enum Kernel { kEmpty, kRegisters, kLanes, kTiles };
+struct Plan {
+  Kernel kernel;
+  int rows, cols, split;
+};
+Plan plan(int64_t rows, int64_t n, int kb, int64_t groups, bool grouped, int sms);
+
 // Up to 8 rows, one group.
 bnn_status gemm_skinny(const Args& a);
 // Tiles of 128 rows (ctas = 1) x 32, 64 or 128 columns, or of 256 rows (a CTA

@@ -369,14 +369,15 @@ bnn_status launch_narrow(const Args& a) {
 }
 
 template <int BN>
-bnn_status narrow(const Args& a) {
+bnn_status narrow(const Args& a, int split) {
   if (a.offsets) return launch_narrow<BN, 1, true>(a);
-  const int64_t tiles = (a.n + kTm - 1) / kTm * ((a.rows + BN - 1) / BN), slots = 2 * bnn::sm_count();
-  if (tiles * 8 <= slots && a.kb >= 16) return launch_narrow<BN, 8, false>(a);
-  if (tiles * 4 <= slots && a.kb >= 8) return launch_narrow<BN, 4, false>(a);
-  if (tiles * 2 <= slots && a.kb >= 4) return launch_narrow<BN, 2, false>(a);
+  if (split == 8) return launch_narrow<BN, 8, false>(a);
+  if (split == 4) return launch_narrow<BN, 4, false>(a);
+  if (split == 2) return launch_narrow<BN, 2, false>(a);
   return launch_narrow<BN, 1, false>(a);
 }
+
+using bnn::fp8::Plan;
 
 // The tile kernel's shape for `rows` rows in `groups` groups: least modelled
 // time, waves x (blocks of k x us a block + us a store), of the shapes that a
@@ -386,33 +387,47 @@ bnn_status narrow(const Args& a) {
 // rows in 64 groups 406 and 404).  A pair's 256 rows end inside the groups (423
 // us there, and 100 against 84 at 4096 rows in 8 groups); in groups of 2048 rows
 // they would save 2%, which is not worth a kernel.
-bnn_status gemm_tiles(const Args& a) {
+Plan plan_tiles(int64_t rows, int64_t n, int kb, int64_t groups, bool grouped, int sms) {
   struct Shape {
     int ctas, tn;
     double block_us, store_us;
   };
   static constexpr Shape kDense[] = {{1, 32, 0.156, 0.4}, {1, 64, 0.19, 0.8}, {1, 128, 0.28, 1.2}, {2, 256, 0.51, 3.0}};
   static constexpr Shape kGrouped[] = {{1, 128, 0.28, 1.2}, {1, 256, 0.51, 3.0}};
-  const bool grouped = a.offsets != nullptr;
   const Shape* shapes = grouped ? kGrouped : kDense;
   const int count = grouped ? 2 : 4;
-  const int64_t sms = bnn::sm_count(), busy = a.rows < a.groups ? a.rows : a.groups;
+  const int64_t busy = rows < groups ? rows : groups;
   const Shape* best = shapes;
   double best_us = 0.0;
   for (int i = 0; i < count; ++i) {
     const Shape& s = shapes[i];
-    const int64_t high = 128 * s.ctas, wide = (a.n + s.tn - 1) / s.tn, slots = sms / s.ctas;
+    const int64_t high = 128 * s.ctas, wide = (n + s.tn - 1) / s.tn, slots = sms / s.ctas;
     // groups end inside a tile, in the mean half a tile each
-    const int64_t rtiles = grouped ? (a.rows + busy * high / 2) / high + 1 : (a.rows + high - 1) / high;
+    const int64_t rtiles = grouped ? (rows + busy * high / 2) / high + 1 : (rows + high - 1) / high;
     const int64_t waves = (rtiles * wide + slots - 1) / slots;
-    const double us = static_cast<double>(waves) * (a.kb * s.block_us + s.store_us);
+    const double us = static_cast<double>(waves) * (kb * s.block_us + s.store_us);
     if (i == 0 || us < best_us) {
       best_us = us;
       best = &s;
     }
   }
-  return bnn::fp8::gemm_tile(a, best->ctas, best->tn);
+  return {bnn::fp8::kTiles, 128 * best->ctas, best->tn, 1};
 }
+
+bnn_status dispatch(const Args& a) {
+  const Plan p = bnn::fp8::plan(a.rows, a.n, a.kb, a.groups, a.offsets != nullptr, bnn::sm_count());
+  switch (p.kernel) {
+    case bnn::fp8::kEmpty: return gemm_empty(a);
+    case bnn::fp8::kRegisters: return bnn::fp8::gemm_skinny(a);
+    case bnn::fp8::kLanes: return p.rows == 16 ? narrow<16>(a, p.split) : narrow<32>(a, p.split);
+    default: return bnn::fp8::gemm_tile(a, p.rows / 128, p.cols);
+  }
+}
+
+}  // namespace
+
+namespace bnn {
+namespace fp8 {
 
 // Few rows (in the mean of the groups: their sizes are on the device): the
 // kernels that stream the weights.  Up to 8 rows and 2^25 bytes of weights the
@@ -420,16 +435,22 @@ bnn_status gemm_tiles(const Args& a) {
 // 2.0 and 3.4, 4096 x 4096 5.6 and 5.9, but 11008 x 4096 11.5 and 11.5, and 28672
 // x 8192 54.7 and 36.4).  Above 32 rows the tile kernel (64 x 11008 x 4096: 13.2
 // us; but 32 x 4096 x 4096 9.3 against 7.7).
-bnn_status dispatch(const Args& a) {
-  if (a.kb == 0) return gemm_empty(a);
-  const int64_t per = (a.rows + a.groups - 1) / a.groups;
-  if (!a.offsets && a.rows <= 8 && a.n * a.kb <= (int64_t{1} << 18)) return bnn::fp8::gemm_skinny(a);
-  if (per <= 16) return narrow<16>(a);
-  if (per <= 32) return narrow<32>(a);
-  return gemm_tiles(a);
+Plan plan(int64_t rows, int64_t n, int kb, int64_t groups, bool grouped, int sms) {
+  if (kb == 0) return {kEmpty, 0, 0, 1};
+  const int64_t per = (rows + groups - 1) / groups;
+  if (!grouped && rows <= 8 && n * kb <= (int64_t{1} << 18)) return {kRegisters, 8, 16, 1};
+  if (per > 32) return plan_tiles(rows, n, kb, groups, grouped, sms);
+  const int bn = per <= 16 ? 16 : 32;
+  int split = 1;
+  if (!grouped) {
+    const int64_t tiles = (n + kTm - 1) / kTm * ((rows + bn - 1) / bn), slots = 2 * sms;
+    split = tiles * 8 <= slots && kb >= 16 ? 8 : tiles * 4 <= slots && kb >= 8 ? 4 : tiles * 2 <= slots && kb >= 4 ? 2 : 1;
+  }
+  return {kLanes, bn, kTm, split};
 }
 
-}  // namespace
+}  // namespace fp8
+}  // namespace bnn
 
 extern "C" bnn_status bnn_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                                    const float* bias, int64_t m, int64_t n, int64_t k, void* out, int out_type,

@@ -2,6 +2,7 @@
 // read-only HBM stream.
 #include "bnn_internal.cuh"
 #include "bnn_probe.h"
+#include "fp8_common.cuh"
 
 namespace {
 
@@ -84,5 +85,19 @@ extern "C" bnn_status bnn_probe_popc(int mode, int64_t blocks, int64_t iters, in
 extern "C" bnn_status bnn_probe_ternary_plan(int64_t n, int64_t k, const int* active, int* rows, int* ks) {
   if (n < 1 || k < 1 || !active || !rows || !ks) return BNN_ERR_INVALID_ARG;
   bnn::ternary_tmem_plan(n, k, active, rows, ks);
+  return BNN_OK;
+}
+
+extern "C" bnn_status bnn_probe_fp8_plan(int64_t rows, int64_t n, int64_t k, int64_t groups, int sms, int* kernel,
+                                         int* tile_rows, int* tile_cols, int* split) {
+  if (rows < 1 || n < 1 || k < 0 || groups < 0 || sms < 2 || rows > INT32_MAX || n > INT32_MAX || k > BNN_MAX_K_FP8 ||
+      groups > BNN_MAX_GROUPS || !kernel || !tile_rows || !tile_cols || !split)
+    return BNN_ERR_INVALID_ARG;
+  const bnn::fp8::Plan p =
+      bnn::fp8::plan(rows, n, static_cast<int>((k + 127) / 128), groups > 0 ? groups : 1, groups > 0, sms);
+  *kernel = p.kernel;
+  *tile_rows = p.rows;
+  *tile_cols = p.cols;
+  *split = p.split;
   return BNN_OK;
 }
