@@ -36,7 +36,7 @@ PLANS = {
     (1, 1024, 1000, 0): (REGISTERS, 8, 16, 1),
     (8, 4096, 8192, 0): (REGISTERS, 8, 16, 1),
     (1, 28672, 1280, 0): (LANES, 16, 128, 1),
-    (5, 28672, 4100, 0): (LANES, 16, 128, 1),
+    (5, 28672, 1200, 0): (LANES, 16, 128, 1),
     (9, 131, 260, 0): (LANES, 16, 128, 1),
     (16, 300, 640, 0): (LANES, 16, 128, 2),
     (12, 400, 1024, 0): (LANES, 16, 128, 4),
