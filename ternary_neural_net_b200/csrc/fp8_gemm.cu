@@ -43,9 +43,12 @@ using bnn::tc::tmem_wait_ld;
 // fetched before the wait for the kernel ahead (not for groups, whose tiles
 // depend on the offsets).
 //
-// Bound by the weights' bytes: 16 x 28672 x 8192 in 37.9 us = 95% of the measured
-// HBM copy (one row 36.4 us = 99%), 512 rows in 64 groups x 2048 x 4096 in 85 us
-// = 97%; small weights by latency (32 x 4096 x 4096 7.7 us, 16 MB in cache).
+// Bound by the weights' bytes: 16 x 28672 x 8192 in 39.8 us = 90% of the measured
+// HBM copy (one row 38.5 us = 93%), 512 rows in 64 groups x 2048 x 4096 in 85 us
+// = 97%; small weights by latency (32 x 4096 x 4096 in 7.4 us = 2.3 TB/s).  Two
+// CTAs an SM leave a thread 128 registers, which 32 rows exceed: ptxas reports 68
+// bytes of spill stores with a split of 4, 120 with 8 and 16 for groups; where
+// they fall has not been looked into.
 // ---------------------------------------------------------------------------
 constexpr int kTm = 128;                    // weight rows of a tile
 constexpr int kBlockBytes = 128;            // bytes of a row's block of k
@@ -381,12 +384,17 @@ using bnn::fp8::Plan;
 
 // The tile kernel's shape for `rows` rows in `groups` groups: least modelled
 // time, waves x (blocks of k x us a block + us a store), of the shapes that a
-// sweep over 64 .. 8192 rows x 4096 .. 11008 x 4096 (and 8192^3) left; the model
-// is within about 10% of what it chooses between.  Groups: 128-row tiles, 128 or
-// 256 columns wide (x 4096 x 4096: 8192 rows in 2 groups 158 and 148 us, 16384
-// rows in 64 groups 406 and 404).  A pair's 256 rows end inside the groups (423
-// us there, and 100 against 84 at 4096 rows in 8 groups); in groups of 2048 rows
-// they would save 2%, which is not worth a kernel.
+// sweep over 64 .. 8192 rows x 4096 .. 11008 x 4096 (and 8192^3) left.  The model
+// orders the shapes and does not tell times: it leaves out what a launch costs
+// (some 4 us), the memory's rate and the power cap, and what is measured is 1-81%
+// above it.  Of 15 sizes measured with every shape it took the fastest in 11, and
+// one 2-9% slower in 4 (2048 x 4096 x 4096: the pair in 45 us, 128 x 128 in 41).
+// Groups: 128-row tiles, 128 or 256 columns wide (x 4096 x 4096, in us: 8192 rows
+// in 2 groups 150 and 149, 16384 in 64 410 and 396; but 8192 in 64 262 and 286,
+// 2048 in 16 66 and 72, where the model takes the wider all the same).  A pair's
+// 256 rows end inside the groups (423 us for 16384 rows in 64, and 100 against 84
+// at 4096 rows in 8); in groups of 2048 rows they would save 2%, which is not
+// worth a kernel.
 Plan plan_tiles(int64_t rows, int64_t n, int kb, int64_t groups, bool grouped, int sms) {
   struct Shape {
     int ctas, tn;
@@ -433,8 +441,12 @@ namespace fp8 {
 // kernels that stream the weights.  Up to 8 rows and 2^25 bytes of weights the
 // register kernel (in us, against the tensor-memory one with 9 rows: 1024 x 1000
 // 2.0 and 3.4, 4096 x 4096 5.6 and 5.9, but 11008 x 4096 11.5 and 11.5, and 28672
-// x 8192 54.7 and 36.4).  Above 32 rows the tile kernel (64 x 11008 x 4096: 13.2
-// us; but 32 x 4096 x 4096 9.3 against 7.7).
+// x 8192 54.7 and 36.4).  Above 32 rows the tile kernel (64 x 11008 x 4096: 14
+// us; but 32 x 4096 x 4096 9.3 against 7.4).  It does not split k, which a long k
+// with few tiles pays for: 32 x 512 x 16384 takes 9-10 us, 33 rows 26, 64 x 1024 x
+// 16384 27.  The mean is of the whole buffer's rows: 64 rows in 64 groups x 2048 x
+// 4096 take 84 us, and 106 (128 x 128 tiles) in a buffer of 4096; 512 rows take 85
+// evenly spread, and 24-27 in one group, in 32 tiles of 16 rows.
 Plan plan(int64_t rows, int64_t n, int kb, int64_t groups, bool grouped, int sms) {
   if (kb == 0) return {kEmpty, 0, 0, 1};
   const int64_t per = (rows + groups - 1) / groups;

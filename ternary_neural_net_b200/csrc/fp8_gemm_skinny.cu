@@ -16,7 +16,7 @@
 // The weights' first blocks are fetched before the wait for the kernel ahead
 // (programmatic dependent launch).
 //
-// 1024 x 1000 in 2.0 us and 4096 x 4096 in 5.6 us back to back, weights in cache;
+// 1024 x 1000 in 2.1 us back to back, weights in cache; 4096 x 4096 in 5.6-6.2 us;
 // 11008 x 4096 in 11.5 us (15.9 us cold: 45.1 MB at 2.8 TB/s, the ramp of so
 // short a launch).  At 28672 x 8192 it runs at 65% of what HBM gives (54.7 us),
 // with 128 registers a thread limiting the bytes in flight, so larger weights go

@@ -24,13 +24,16 @@
 // iteration into the SM, 1024 clocks at the 64 bytes a clock that an SM reads
 // from L2, and takes 950-1000; a pair's 256 x 256 moves 32 KiB, and its epilogue
 // (128 columns a thread, two warps in each sub-partition: loads of tensor memory
-// and multiply-adds that wait for them) takes about 930.  That is 0.48 ms at
-// 8192^3 = 2280 TFLOP/s while the clock holds and 0.54 ms back to back under the
-// power cap.  Tried there: sixteen epilogue warps (0.55 ms), 32-column loads or
-// the next iteration's loads ahead of this one's end (0.51-0.58 ms: registers
-// spill), scalar multiply-adds (0.49 ms), 256 x 192 tiles (0.53-0.59 ms, the same
-// with four loads in flight and with six: the epilogue takes some 2.9 clocks a
-// column and 220 a block whatever is in flight).
+// and multiply-adds that wait for them) takes about 930: neither the multiply-adds
+// (256 clocks of them) nor the tensor cores are full, and which wait it is that
+// adds up has not been measured.  8192^3 takes 0.57-0.58 ms = 1900 TFLOP/s with
+// normally distributed values, under the power cap (1480-1790 MHz sampled of
+// 1965); short bursts of uniform positive codes, which draw less, 0.48-0.51 ms.
+// Tried in such bursts (0.48 ms): sixteen epilogue warps (0.55 ms), 32-column
+// loads or the next iteration's loads ahead of this one's end (0.51-0.58 ms:
+// registers spill), scalar multiply-adds (0.49 ms), 256 x 192 tiles (0.53-0.59 ms,
+// the same with four loads in flight and with six: the epilogue takes some 2.9
+// clocks a column and 220 a block whatever is in flight).
 //
 // Roles per CTA: warps 0-7 epilogue (lane quarter w % 4, column half w / 4),
 // warp 8 TMA, warp 9 MMA (CTA 0's issues for a pair), warps 10 and 11 the

@@ -13,9 +13,10 @@
 //
 // Both kernels are bound by HBM (2 or 4 bytes read and 1 written per element):
 // every element is read once, kept in registers over the maximum, and written
-// once.  Rows of 8192 x 8192: bfloat16 33-35 us (87-92% of the measured copy),
-// float32 53.7 us (95%).  Weights: 11008 x 4096 float32 35.5 us (97%), 16384 x
-// 8192 bfloat16 63.5 us (97%).
+// once.  Rows of 8192 x 8192: bfloat16 33 us (94% of the measured copy; 36 held
+// under the power cap), float32 53.7 us (95%).  Weights: 11008 x 4096 float32
+// 35-38 us (91-98%), 16384 x 8192 bfloat16 63.5 us (97%), 8 x 2050 x 4100 bfloat16
+// (rows of 8-byte alignment, 2050 = 16 x 128 + 2) 44 us (71%).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -193,7 +194,8 @@ fp8_pack_rows_kernel(const T* __restrict__ x, int64_t x_rows, const int32_t* __r
 }
 
 // Weights.  A CTA takes 128 rows x kBlocks blocks (512 bytes of a row) whole in
-// registers, a warp 16 of the rows, one 16-byte load a lane for each.
+// registers, a warp 16 of the rows, one 16-byte load a lane for each.  (2-byte
+// loads spill 68 bytes a thread at two CTAs an SM, the wide ones 16 at three.)
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, V * sizeof(T) >= 8 ? 3 : 2)
 fp8_pack_weight_kernel(const T* __restrict__ w, int64_t n, int64_t k, int64_t kb, int64_t nb, int64_t col_tiles,
