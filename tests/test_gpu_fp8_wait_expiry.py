@@ -14,14 +14,19 @@ from ternary_neural_net_b200 import synth
 
 pytestmark = pytest.mark.gpu
 
-# (m, n, k, groups): each kernel and shape that a call can take on this device (148 SMs)
+# (m, n, k, groups): each kernel and shape with waits (test_fp8_plan.py has the kernel of each size)
 CASES = [
     (16, 300, 640, 0),        # weights on the lanes, 16 rows, split over 2 CTAs
     (12, 400, 1024, 0),       # 4 CTAs
-    (20, 500, 8192, 0),       # 32 rows, 8 CTAs
-    (30, 40000, 300, 0),      # no split, several tiles a CTA
+    (16, 1000, 8192, 0),      # 8 CTAs
+    (16, 40000, 300, 0),      # no split, several tiles a CTA
+    (24, 300, 640, 0),        # 32 rows, 2 CTAs
+    (24, 400, 1024, 0),       # 4 CTAs
+    (20, 500, 8192, 0),       # 8 CTAs
+    (30, 40000, 300, 0),      # no split
     (64, 1000, 8192, 0),      # 128 x 32 tiles
-    (300, 2000, 4100, 0),     # 128 x 64 or 128 x 128
+    (300, 2000, 4100, 0),     # 128 x 64
+    (3000, 9100, 1100, 0),    # 128 x 128, several tiles each
     (1101, 2304, 2000, 0),    # CTA pairs, 256 x 256
     (2048, 4600, 2000, 0),    # pairs, several tiles each
     (200, 300, 2000, 20),     # groups, 16 rows
